@@ -72,7 +72,8 @@ extern "C" {
 #define SCONV_KV_ERR_ALIGN (-3)       /* pointer or stride not 16-byte aligned */
 #define SCONV_KV_ERR_UNSUPPORTED (-4) /* valid but not implemented combination */
 #define SCONV_KV_ERR_CUDA (-5)        /* CUDA reported an error at launch     */
-#define SCONV_KV_ERR_SCRATCH (-6)     /* call needs more than the static scratch */
+#define SCONV_KV_ERR_SCRATCH (-6)     /* call needs more than the static scratch
+                                         or the given workspace              */
 
 /* ---------------------------------------------------- device-side flag bits */
 #define SCONV_KV_FLAG_SLOT_RANGE 1   /* slot >= num_pages*page_size: skipped  */
@@ -83,9 +84,17 @@ extern "C" {
 #define SCONV_KV_FLAG_TIMEOUT 8      /* an internal pipeline wait gave up after
                                         its time limit (about 1 s): the CTA
                                         stopped early, output incomplete      */
+#define SCONV_KV_FLAG_TREE 16        /* a malformed tree of drafted tokens: a
+                                        parent at or behind its child, or an
+                                        unused one; more than max_draft tokens;
+                                        a leaf that is no used token          */
+#define SCONV_KV_FLAG_CONTEXT 32     /* a context length below 0, or more tokens
+                                        than the block table's row has slots:
+                                        sequence skipped                      */
 
 /* ------------------------------------------------------------- limits */
 #define SCONV_KV_MAX_W 8             /* conv width W in [1, SCONV_KV_MAX_W]   */
+#define SCONV_KV_MAX_DRAFT 128       /* drafted tokens of one sequence         */
 
 /*
  * Paged KV cache layout.  Element (slot, h, d) of k_cache (and of v_cache)
@@ -452,6 +461,218 @@ SCONV_KV_API int sconv_kv_unfused_step_noalloc(
     const int32_t* state_indices, int64_t state_pool_size,
     const int64_t* slot_mapping, void* k_cache, void* v_cache,
     const sconv_kv_cache_layout_t* layout, int* err_flag, void* stream);
+
+/*
+ * Drafted trees over the paged cache (speculative decoding; a tree of one
+ * token is the plain decode) and eviction from the cache.  The source pages
+ * name neither: these entry points read and maintain the cache that the
+ * step writes, for a serving runtime around it.  One serving step is
+ *
+ *   sconv_kv_tree_step          K/V rows of the drafted tokens into the cache
+ *   sconv_kv_tree_attention     their attention over context and tree
+ *   sconv_kv_attention_weights  (optional) weight of every cached row
+ *   sconv_kv_tree_accept        the accepted path becomes context
+ *   sconv_kv_evict              (now and then) rows of least weight leave
+ *
+ * Sequence i holds context_lens[i] cached tokens at positions
+ * 0 .. context_lens[i]-1.  Its drafted tokens are packed tokens
+ * cu_draft[i] .. cu_draft[i+1]-1; the j-th lies at position
+ * context_lens[i] + j.  Position p is slot p % page_size of page
+ * block_table[i, p / page_size].  parents[t] is the local index (within the
+ * sequence, below its own) of the token that drafted token t follows; -1:
+ * it follows the context; <= -2: unused (padding): nothing sees it, it
+ * sees nothing.  A token whose parents do not end at -1 counts as unused,
+ * and SCONV_KV_FLAG_TREE is set.  Tokens behind cu_draft[num_seqs] are left
+ * alone.
+ *
+ * A sequence that cannot be processed (malformed cu_draft, more than
+ * max_draft tokens, bad context length) is skipped, its outputs left as they
+ * were, and flagged.  A page outside the cache sets
+ * SCONV_KV_FLAG_SLOT_RANGE: no out-of-range memory is touched, rows are not
+ * moved from or to it, and the attention outputs and weights of that sequence are
+ * unspecified.
+ */
+typedef struct sconv_kv_paged_t {
+  const int32_t* cu_draft;     /* device [num_seqs + 1]; unused by evict      */
+  const int32_t* parents;      /* device [num_tokens]; unused by evict        */
+  int64_t num_tokens;          /* rows of the packed drafted tensors          */
+  int32_t num_seqs;
+  int32_t max_draft;           /* most drafted tokens of a sequence, 1 ..
+                                  SCONV_KV_MAX_DRAFT (a host-side bound)      */
+  const int32_t* context_lens; /* device [num_seqs]                           */
+  const int32_t* block_table;  /* device [num_seqs, table_width]              */
+  int64_t table_width;         /* pages a row; width * page_size < 2^31       */
+  int64_t table_stride;        /* elements between rows, >= table_width       */
+} sconv_kv_paged_t;
+
+/*
+ * The ShortConv K/V step for drafted trees: as sconv_kv_prefill_varlen, with
+ * each token's window going up its parents and then into the sequence's
+ * conv_state, which is only read (sconv_kv_tree_accept advances it).  A
+ * chain gives the bits of the prefill and decode entry points.  Unused
+ * tokens are not written; a token with a malformed parent within its window
+ * is not written and flagged.  `options`: NULL, or per-head gammas and a
+ * ring state as in the _ex entry points (the other fields are not used).
+ * The _mxfp8 twin stores as sconv_kv_prefill_varlen_mxfp8.
+ */
+SCONV_KV_API int sconv_kv_tree_step(
+    const void* k, const void* v, int64_t row_stride, int64_t num_tokens,
+    const int32_t* cu_draft, const int32_t* parents, int num_seqs,
+    const void* conv_w_k, const void* conv_w_v, const float* gamma_k,
+    const float* gamma_v, float eps, int W, int num_kv_heads, int head_dim,
+    const void* conv_state, const int32_t* state_indices,
+    int64_t state_pool_size, const int64_t* slot_mapping, void* k_cache,
+    void* v_cache, const sconv_kv_cache_layout_t* layout,
+    const sconv_kv_options_t* options, int* err_flag, void* stream);
+
+SCONV_KV_API int sconv_kv_tree_step_mxfp8(
+    const void* k, const void* v, int64_t row_stride, int64_t num_tokens,
+    const int32_t* cu_draft, const int32_t* parents, int num_seqs,
+    const void* conv_w_k, const void* conv_w_v, const float* gamma_k,
+    const float* gamma_v, float eps, int W, int num_kv_heads, int head_dim,
+    const void* conv_state, const int32_t* state_indices,
+    int64_t state_pool_size, const int64_t* slot_mapping, void* k_data,
+    uint8_t* k_scale, void* v_data, uint8_t* v_scale,
+    const sconv_kv_cache_layout_t* layout, const sconv_kv_options_t* options,
+    int* err_flag, void* stream);
+
+/*
+ * Attention of the drafted tokens over their context and their ancestors:
+ * with s_p = scale * q . k_p over the positions p that token t sees (the
+ * context, its ancestors and itself),
+ *     out[t, hq] = sum_p softmax(s)_p v_p,    lse[t, hq] = ln sum_p exp(s_p)
+ * K/V head of query head hq: hq / (num_q_heads / num_kv_heads).  An unused
+ * token gets out = 0, lse = -inf.  NaN and infinities in rows that a token
+ * does not see do not reach it.  fp32 scores, statistics and sums; the
+ * probabilities are rounded to bf16 for the second product.  The same call
+ * gives the same bits.
+ *
+ *  q          bf16, head hq of token t at q + t*q_token_stride +
+ *             hq*q_head_stride; strides multiples of 8, 16-byte aligned.
+ *  out        bf16, likewise; must not alias q.
+ *  lse        fp32 [num_tokens, num_q_heads] or NULL.
+ *  workspace  device scratch of at least the bytes that
+ *             sconv_kv_tree_attention_workspace names, 16-byte aligned, with
+ *             any contents; calls (and replays of captured calls) that may
+ *             overlap on the GPU need workspaces of their own.  Too small:
+ *             SCONV_KV_ERR_SCRATCH.
+ * num_q_heads must be a multiple of num_kv_heads; head_dim 64, 128 or 256.
+ * Cache strides as for the step (_mxfp8: multiples of 32).
+ */
+SCONV_KV_API int sconv_kv_tree_attention_workspace(
+    int num_seqs, int max_draft, int num_q_heads, int num_kv_heads,
+    int head_dim, int64_t* bytes);
+
+SCONV_KV_API int sconv_kv_tree_attention(
+    const void* q, int64_t q_token_stride, int64_t q_head_stride,
+    int num_q_heads, int num_kv_heads, int head_dim, float scale,
+    const sconv_kv_paged_t* seqs, const void* k_cache, const void* v_cache,
+    const sconv_kv_cache_layout_t* layout, void* out, int64_t out_token_stride,
+    int64_t out_head_stride, float* lse, void* workspace,
+    int64_t workspace_bytes, int* err_flag, void* stream);
+
+SCONV_KV_API int sconv_kv_tree_attention_mxfp8(
+    const void* q, int64_t q_token_stride, int64_t q_head_stride,
+    int num_q_heads, int num_kv_heads, int head_dim, float scale,
+    const sconv_kv_paged_t* seqs, const void* k_data, const uint8_t* k_scale,
+    const void* v_data, const uint8_t* v_scale,
+    const sconv_kv_cache_layout_t* layout, void* out, int64_t out_token_stride,
+    int64_t out_head_stride, float* lse, void* workspace,
+    int64_t workspace_bytes, int* err_flag, void* stream);
+
+/*
+ * Accumulated attention weights, the score that sconv_kv_evict goes by.
+ * weights is fp32, position p < positions of head h of sequence i at
+ * weights + i*seq_stride + h*head_stride + p; a sequence with more tokens than
+ * that is skipped and flagged (SCONV_KV_FLAG_CONTEXT; so too in
+ * sconv_kv_tree_accept and sconv_kv_evict).  With add = sum over the used drafted tokens that
+ * see p, and the query heads of h, of exp(scale * q . k_p - lse),
+ *     weights += add  for p < context_lens[i],
+ *     weights  = add  for the rows of drafted tokens (a new row starts here).
+ * lse is what sconv_kv_tree_attention gave.  To count accepted tokens only,
+ * pass parents in which the others are -2.  Arguments otherwise as above;
+ * the V cache is not read.
+ */
+SCONV_KV_API int sconv_kv_attention_weights(
+    const void* q, int64_t q_token_stride, int64_t q_head_stride,
+    int num_q_heads, int num_kv_heads, int head_dim, float scale,
+    const float* lse, const sconv_kv_paged_t* seqs, const void* k_cache,
+    const sconv_kv_cache_layout_t* layout, float* weights, int64_t positions,
+    int64_t seq_stride, int64_t head_stride, int* err_flag, void* stream);
+
+SCONV_KV_API int sconv_kv_attention_weights_mxfp8(
+    const void* q, int64_t q_token_stride, int64_t q_head_stride,
+    int num_q_heads, int num_kv_heads, int head_dim, float scale,
+    const float* lse, const sconv_kv_paged_t* seqs, const void* k_data,
+    const uint8_t* k_scale, const sconv_kv_cache_layout_t* layout,
+    float* weights, int64_t positions, int64_t seq_stride,
+    int64_t head_stride, int* err_flag, void* stream);
+
+/*
+ * Accept one path of each tree.  leaves[i] (device int32) is the local index
+ * of the path's last token, -1: nothing is accepted.  With the path
+ * a_0 < ... < a_{m-1} (the leaf's ancestors and the leaf), the cache row (and,
+ * where weights is not NULL, the weight) of position ctx + a_r moves to
+ * ctx + r, the conv_state takes the last W-1 rows of (state ++ the path's raw
+ * k/v rows), and new_lens[i] = ctx + m.  k, v, row_stride: the raw rows given to
+ * sconv_kv_tree_step.  new_lens must not alias context_lens.  W == 1: no state.
+ * state_positions (device int64 [num_seqs], or NULL) selects the ring state as in
+ * sconv_kv_options_t: tokens seen before the path.  A bad leaf accepts
+ * nothing (new_lens = ctx) and is flagged; a bad state index or negative
+ * position leaves the state and is flagged.
+ */
+SCONV_KV_API int sconv_kv_tree_accept(
+    const void* k, const void* v, int64_t row_stride,
+    const sconv_kv_paged_t* seqs, const int32_t* leaves, int W,
+    int num_kv_heads, int head_dim, void* conv_state,
+    const int32_t* state_indices, int64_t state_pool_size,
+    const int64_t* state_positions, void* k_cache, void* v_cache,
+    const sconv_kv_cache_layout_t* layout, float* weights, int64_t positions,
+    int64_t seq_stride, int64_t head_stride, int32_t* new_lens, int* err_flag,
+    void* stream);
+
+SCONV_KV_API int sconv_kv_tree_accept_mxfp8(
+    const void* k, const void* v, int64_t row_stride,
+    const sconv_kv_paged_t* seqs, const int32_t* leaves, int W,
+    int num_kv_heads, int head_dim, void* conv_state,
+    const int32_t* state_indices, int64_t state_pool_size,
+    const int64_t* state_positions, void* k_data, uint8_t* k_scale,
+    void* v_data, uint8_t* v_scale, const sconv_kv_cache_layout_t* layout,
+    float* weights, int64_t positions, int64_t seq_stride,
+    int64_t head_stride, int32_t* new_lens, int* err_flag, void* stream);
+
+/*
+ * Evict rows from the cache, each K/V head by its own weights.  A sequence
+ * with context_lens[i] > keep keeps its first `sinks` and last `recent`
+ * positions and, of the others, the keep - sinks - recent of the largest
+ * weight (equal weights: the lower position; -0 equals 0, NaN is above all).  The
+ * kept rows move, in place, to positions 0 .. keep-1 in their order;
+ *   kept[i, h, r]   int32 [num_seqs, num_kv_heads, keep]: the old position of
+ *                   row r; -1 behind a shorter sequence's rows;
+ *   new_lens[i]     min(context_lens[i], keep); must not alias context_lens;
+ *   weights_out     NULL, or fp32 like weights with strides of its own: the kept rows'
+ *                   weights at 0 .. new_lens[i]-1 (the rest as it was); must
+ *                   not alias weights; out_positions >= min(keep, positions).
+ * keep >= 1, sinks and recent >= 0, sinks + recent <= keep, else
+ * SCONV_KV_ERR_SHAPE.  Two sequences that share a page (a common prefix) must
+ * not be evicted in place: results are then unspecified.
+ */
+SCONV_KV_API int sconv_kv_evict(
+    const float* weights, int64_t positions, int64_t seq_stride,
+    int64_t head_stride, const sconv_kv_paged_t* seqs, int keep, int sinks, int recent,
+    int num_kv_heads, int head_dim, void* k_cache, void* v_cache,
+    const sconv_kv_cache_layout_t* layout, int32_t* kept, int32_t* new_lens,
+    float* weights_out, int64_t out_positions, int64_t out_seq_stride,
+    int64_t out_head_stride, int* err_flag, void* stream);
+
+SCONV_KV_API int sconv_kv_evict_mxfp8(
+    const float* weights, int64_t positions, int64_t seq_stride,
+    int64_t head_stride, const sconv_kv_paged_t* seqs, int keep, int sinks, int recent,
+    int num_kv_heads, int head_dim, void* k_data, uint8_t* k_scale,
+    void* v_data, uint8_t* v_scale, const sconv_kv_cache_layout_t* layout,
+    int32_t* kept, int32_t* new_lens, float* weights_out,
+    int64_t out_positions, int64_t out_seq_stride, int64_t out_head_stride,
+    int* err_flag, void* stream);
 
 /* Static text for a status code (never NULL). */
 SCONV_KV_API const char* sconv_kv_strerror(int status);

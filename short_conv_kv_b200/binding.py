@@ -21,7 +21,9 @@ OK = 0
 ERR_NULL, ERR_SHAPE, ERR_ALIGN, ERR_UNSUPPORTED, ERR_CUDA, ERR_SCRATCH = -1, -2, -3, -4, -5, -6
 NOALLOC_SCRATCH_BYTES = 64 << 20
 FLAG_SLOT_RANGE, FLAG_STATE_INDEX, FLAG_CU_SEQLENS, FLAG_TIMEOUT = 1, 2, 4, 8
+FLAG_TREE, FLAG_CONTEXT = 16, 32
 MAX_W = 8
+MAX_DRAFT = 128
 
 
 class CacheLayout(ctypes.Structure):
@@ -35,6 +37,15 @@ class Options(ctypes.Structure):
     _fields_ = [("gamma_head_stride", ctypes.c_int64), ("state_positions", ctypes.c_void_p),
                 ("wait_timeout_ns", ctypes.c_int64), ("withhold_first_copy", ctypes.c_int64),
                 ("state_only_dependency", ctypes.c_int64), ("independent_state", ctypes.c_int64)]
+
+
+class Paged(ctypes.Structure):
+    """sconv_kv_paged_t: paged sequences with their drafted tokens."""
+    _fields_ = [("cu_draft", ctypes.c_void_p), ("parents", ctypes.c_void_p),
+                ("num_tokens", ctypes.c_int64), ("num_seqs", ctypes.c_int32),
+                ("max_draft", ctypes.c_int32), ("context_lens", ctypes.c_void_p),
+                ("block_table", ctypes.c_void_p), ("table_width", ctypes.c_int64),
+                ("table_stride", ctypes.c_int64)]
 
 
 class SconvKVError(RuntimeError):
@@ -105,6 +116,31 @@ def _load(path):
         vp, vp, i64, i64, vp, i32, vp, vp, vp, vp, f32, i32, i32, i32, vp, vp,
         i64, vp, vp, vp, lp, ip, vp]
     lib.sconv_kv_unfused_step_noalloc.restype = i32
+    pp = ctypes.POINTER(Paged)
+    step = [vp, vp, i64, i64, vp, vp, i32, vp, vp, vp, vp, f32, i32, i32, i32, vp, vp, i64, vp]
+    lib.sconv_kv_tree_step.argtypes = step + [vp, vp, lp, op, ip, vp]
+    lib.sconv_kv_tree_step_mxfp8.argtypes = step + [vp, vp, vp, vp, lp, op, ip, vp]
+    lib.sconv_kv_tree_attention_workspace.argtypes = [i32, i32, i32, i32, i32,
+                                                      ctypes.POINTER(i64)]
+    att = [vp, i64, i64, i32, i32, i32, f32]
+    lib.sconv_kv_tree_attention.argtypes = att + [pp, vp, vp, lp, vp, i64, i64, vp, vp, i64, ip, vp]
+    lib.sconv_kv_tree_attention_mxfp8.argtypes = att + [pp, vp, vp, vp, vp, lp, vp, i64, i64, vp,
+                                                        vp, i64, ip, vp]
+    lib.sconv_kv_attention_weights.argtypes = att + [vp, pp, vp, lp, vp, i64, i64, i64, ip,
+                                                     vp]
+    lib.sconv_kv_attention_weights_mxfp8.argtypes = att + [vp, pp, vp, vp, lp, vp, i64, i64,
+                                                           i64, ip, vp]
+    acc = [vp, vp, i64, pp, vp, i32, i32, i32, vp, vp, i64, vp]
+    lib.sconv_kv_tree_accept.argtypes = acc + [vp, vp, lp, vp, i64, i64, i64, vp, ip, vp]
+    lib.sconv_kv_tree_accept_mxfp8.argtypes = acc + [vp, vp, vp, vp, lp, vp, i64, i64, i64, vp,
+                                                     ip, vp]
+    evi = [vp, i64, i64, i64, pp, i32, i32, i32, i32, i32]
+    lib.sconv_kv_evict.argtypes = evi + [vp, vp, lp, vp, vp, vp, i64, i64, i64, ip, vp]
+    lib.sconv_kv_evict_mxfp8.argtypes = evi + [vp, vp, vp, vp, lp, vp, vp, vp, i64, i64, i64, ip, vp]
+    for n in ("tree_step", "tree_attention", "attention_weights", "tree_accept", "evict"):
+        getattr(lib, "sconv_kv_" + n).restype = i32
+        getattr(lib, "sconv_kv_" + n + "_mxfp8").restype = i32
+    lib.sconv_kv_tree_attention_workspace.restype = i32
     lib.sconv_kv_strerror.argtypes = [i32]
     lib.sconv_kv_strerror.restype = ctypes.c_char_p
     lib.sconv_kv_last_cuda_error.argtypes = []
@@ -576,3 +612,330 @@ def unfused_step_noalloc(k, v, cu_seqlens, conv_w_k, conv_w_v, gamma_k, gamma_v,
         _ptr(conv_state) if W > 1 else None, _ptr(state_indices), pool, _ptr(slot_mapping),
         _ptr(k_cache), _ptr(v_cache), ctypes.byref(lay), _ptr(err_flag), _stream(stream)),
         "sconv_kv_unfused_step_noalloc")
+
+
+# ------------------------------------------- drafted trees, and the cache's eviction
+
+_I32, _F32, _BF16 = torch.int32, torch.float32, torch.bfloat16
+
+
+def _same_device(dev, **tensors):
+    if dev.type != "cuda":
+        raise ValueError("the tensors must be on a CUDA device")
+    for name, t in tensors.items():
+        if t is not None and t.device != dev:
+            raise ValueError(f"{name} is on {t.device}, not on {dev}")
+
+
+def _dense(t, name, dtype, shape):
+    """Check a contiguous tensor of the given type and shape."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {str(dtype)[6:]}")
+    if tuple(t.shape) != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous {list(shape)}, not {list(t.shape)}")
+
+
+def _on(dev, stream, name, *args):
+    """Call the C entry point with dev current, on `stream` or dev's current one."""
+    if stream is None:
+        s = torch.cuda.current_stream(dev).cuda_stream
+    else:
+        s = _stream(stream)
+    fn = getattr(_lib, name)
+    if torch.cuda.current_device() == dev.index:
+        rc = fn(*args, s)
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(*args, s)
+    if rc != OK:
+        raise SconvKVError(rc, name)
+
+
+def _paged(context_lens, block_table, cu_draft=None, parents=None, num_tokens=0, max_draft=0):
+    if block_table.dtype != _I32 or block_table.dim() != 2 or block_table.stride(1) != 1:
+        raise TypeError("block_table must be int32 [num_seqs, pages] with unit page stride")
+    S = block_table.shape[0]
+    _dense(context_lens, "context_lens", _I32, (S,))
+    p = Paged()
+    if cu_draft is not None:
+        _dense(cu_draft, "cu_draft", _I32, (S + 1,))
+        _dense(parents, "parents", _I32, (num_tokens,))
+        p.cu_draft, p.parents = cu_draft.data_ptr(), parents.data_ptr()
+        p.num_tokens, p.max_draft = num_tokens, int(max_draft)
+    p.num_seqs = S
+    p.context_lens, p.block_table = context_lens.data_ptr(), block_table.data_ptr()
+    p.table_width = block_table.shape[1]
+    p.table_stride = max(block_table.stride(0), block_table.shape[1])
+    return p
+
+
+def _cache_pair(k_cache, v_cache):
+    if k_cache.dtype != _BF16 or (v_cache is not None and v_cache.dtype != _BF16):
+        raise TypeError("caches must be bfloat16")
+    if v_cache is not None and (v_cache.stride() != k_cache.stride() or
+                                v_cache.shape != k_cache.shape):
+        raise ValueError("k_cache and v_cache must have the same shape and strides")
+    return layout_of(k_cache)
+
+
+def _query(q, name):
+    if q.dtype != _BF16:
+        raise TypeError(f"{name} must be bfloat16")
+    if q.dim() != 3 or q.stride(2) != 1:
+        raise ValueError(f"{name} must be [T, Hq, D] with unit dim stride")
+    T, H, D = q.shape
+    # a dimension of size 1 has a stride of its own making
+    sh = q.stride(1) if H > 1 else D
+    st = q.stride(0) if T > 1 else max(q.stride(0), H * D)
+    return q.data_ptr(), st, sh
+
+
+def _weight_rows(weights, name, S, H):
+    """(pointer, positions, sequence stride, head stride) of fp32 [S, Hkv, positions]."""
+    if weights.dtype != _F32:
+        raise TypeError(f"{name} must be float32")
+    if weights.dim() != 3 or weights.shape[0] != S or weights.shape[1] != H or weights.stride(2) != 1:
+        raise ValueError(f"{name} must be [{S}, {H}, positions] with unit position stride")
+    return weights.data_ptr(), weights.shape[2], weights.stride(0), weights.stride(1)
+
+
+def _tree_step(name, k, v, cu_draft, parents, conv_w_k, conv_w_v, gamma_k, gamma_v, eps,
+               conv_state, slot_mapping, cache, lay, state_indices, state_positions, err_flag,
+               stream):
+    kp, rs = _rows(k, "k")
+    vp, rs_v = _rows(v, "v")
+    if rs != rs_v or v.shape != k.shape:
+        raise ValueError("k and v must share shape and row stride")
+    T, S, W = k.shape[0], cu_draft.shape[0] - 1, conv_w_k.shape[0]
+    _same_device(k.device, v=v, cu_draft=cu_draft, parents=parents, slot_mapping=slot_mapping,
+                 k_cache=cache[0], conv_state=conv_state, state_indices=state_indices)
+    _dense(cu_draft, "cu_draft", _I32, (S + 1,))
+    _dense(parents, "parents", _I32, (T,))
+    _dense(slot_mapping, "slot_mapping", torch.int64, (T,))
+    if state_indices is not None:
+        _dense(state_indices, "state_indices", _I32, (S,))
+    opts = _options(gamma_k, state_positions)
+    _on(k.device, stream, name, kp, vp, rs, T, cu_draft.data_ptr(), parents.data_ptr(), S,
+        _ptr(conv_w_k), _ptr(conv_w_v), _ptr(gamma_k), _ptr(gamma_v), float(eps), W,
+        lay.num_kv_heads, lay.head_dim, _ptr(conv_state) if W > 1 else None, _ptr(state_indices),
+        conv_state.shape[0] if conv_state is not None else 0, slot_mapping.data_ptr(),
+        *(t.data_ptr() for t in cache), ctypes.byref(lay),
+        None if opts is None else ctypes.byref(opts), _ptr(err_flag))
+
+
+def tree_step(k, v, cu_draft, parents, conv_w_k, conv_w_v, gamma_k, gamma_v, eps, conv_state,
+              slot_mapping, k_cache, v_cache, state_indices=None, err_flag=None, stream=None,
+              state_positions=None):
+    """The ShortConv K/V step for trees of drafted tokens: token t's conv
+    window goes up its parents (int32 [T], local indices; -1 the context,
+    <= -2 unused) and then into conv_state, which is only read.  cu_draft:
+    int32 [S+1]; the rest as in prefill_varlen."""
+    _tree_step("sconv_kv_tree_step", k, v, cu_draft, parents, conv_w_k, conv_w_v, gamma_k, gamma_v,
+               eps, conv_state, slot_mapping, (k_cache, v_cache), _cache_pair(k_cache, v_cache),
+               state_indices, state_positions, err_flag, stream)
+
+
+def tree_step_mxfp8(k, v, cu_draft, parents, conv_w_k, conv_w_v, gamma_k, gamma_v, eps, conv_state,
+                    slot_mapping, k_data, k_scale, v_data, v_scale, state_indices=None,
+                    err_flag=None, stream=None, state_positions=None):
+    """tree_step with the MXFP8 cache store."""
+    _tree_step("sconv_kv_tree_step_mxfp8", k, v, cu_draft, parents, conv_w_k, conv_w_v, gamma_k,
+               gamma_v, eps, conv_state, slot_mapping, (k_data, k_scale, v_data, v_scale),
+               _mx_layout(k_data, k_scale, v_data, v_scale), state_indices, state_positions,
+               err_flag, stream)
+
+
+def tree_attention_workspace(q, k_cache, num_seqs, max_draft):
+    """A workspace (uint8, on q's device) for tree_attention calls with up to
+    num_seqs sequences of up to max_draft drafted tokens, q's heads and
+    k_cache's (bf16 or MXFP8 codes) heads and head_dim.  Calls that may
+    overlap on the GPU need one each."""
+    _same_device(q.device, k_cache=k_cache)
+    need = ctypes.c_int64()
+    args = (int(num_seqs), int(max_draft), q.shape[1], k_cache.shape[2], k_cache.shape[3],
+            ctypes.byref(need))
+    with torch.cuda.device(q.device):
+        _check(_lib.sconv_kv_tree_attention_workspace(*args), "sconv_kv_tree_attention_workspace")
+    return torch.empty(need.value, dtype=torch.uint8, device=q.device)
+
+
+def _tree_attention(name, q, cu_draft, parents, context_lens, block_table, cache, lay, scale,
+                    max_draft, out, lse, workspace, err_flag, stream):
+    T, HQ = q.shape[0], q.shape[1]
+    qp, qt, qh = _query(q, "q")
+    if q.shape[2] != lay.head_dim:
+        raise ValueError("q and the cache differ in head_dim")
+    if out is None:
+        out = torch.empty(q.shape, dtype=_BF16, device=q.device)
+    if out.shape != q.shape:
+        raise ValueError("out must have q's shape")
+    op, ot, oh = _query(out, "out")
+    if lse is not None:
+        _dense(lse, "lse", _F32, (T, HQ))
+    seqs = _paged(context_lens, block_table, cu_draft, parents, T, max_draft)
+    if workspace is None:
+        workspace = tree_attention_workspace(q, cache[0], seqs.num_seqs, max_draft)
+    elif not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    _same_device(q.device, cu_draft=cu_draft, parents=parents, context_lens=context_lens,
+                 block_table=block_table, cache=cache[0], out=out, lse=lse, workspace=workspace)
+    _on(q.device, stream, name, qp, qt, qh, HQ, lay.num_kv_heads, lay.head_dim, float(scale),
+        ctypes.byref(seqs), *(t.data_ptr() for t in cache), ctypes.byref(lay), op, ot, oh,
+        _ptr(lse), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+        _ptr(err_flag))
+    return out
+
+
+def tree_attention(q, cu_draft, parents, context_lens, block_table, k_cache, v_cache, scale,
+                   max_draft, out=None, lse=None, workspace=None, err_flag=None, stream=None):
+    """Attention of drafted tokens (q bf16 [T, Hq, D], packed by cu_draft) over
+    their paged context and their ancestors in the tree.  context_lens int32
+    [S]; block_table int32 [S, pages]; draft j of sequence i lies at position
+    context_lens[i] + j.  max_draft: a host-side bound on the drafted tokens
+    of a sequence.  Writes and returns out (bf16, q's shape) and fills lse
+    (fp32 [T, Hq], natural logarithm) if given.  A chain of one token is the
+    plain decode.  Pass a workspace (tree_attention_workspace) to allocate
+    nothing, and under graph capture."""
+    return _tree_attention("sconv_kv_tree_attention", q, cu_draft, parents, context_lens,
+                           block_table, (k_cache, v_cache), _cache_pair(k_cache, v_cache), scale,
+                           max_draft, out, lse, workspace, err_flag, stream)
+
+
+def tree_attention_mxfp8(q, cu_draft, parents, context_lens, block_table, k_data, k_scale, v_data,
+                         v_scale, scale, max_draft, out=None, lse=None, workspace=None,
+                         err_flag=None, stream=None):
+    """tree_attention over an MXFP8 cache."""
+    return _tree_attention("sconv_kv_tree_attention_mxfp8", q, cu_draft, parents, context_lens,
+                           block_table, (k_data, k_scale, v_data, v_scale),
+                           _mx_layout(k_data, k_scale, v_data, v_scale), scale, max_draft, out,
+                           lse, workspace, err_flag, stream)
+
+
+def _attention_weights(name, q, lse, cu_draft, parents, context_lens, block_table, cache, lay,
+                       scale, max_draft, weights, err_flag, stream):
+    T, HQ = q.shape[0], q.shape[1]
+    qp, qt, qh = _query(q, "q")
+    if q.shape[2] != lay.head_dim:
+        raise ValueError("q and the cache differ in head_dim")
+    _dense(lse, "lse", _F32, (T, HQ))
+    seqs = _paged(context_lens, block_table, cu_draft, parents, T, max_draft)
+    wargs = _weight_rows(weights, "weights", seqs.num_seqs, lay.num_kv_heads)
+    _same_device(q.device, lse=lse, cu_draft=cu_draft, parents=parents, context_lens=context_lens,
+                 block_table=block_table, cache=cache[0], weights=weights)
+    _on(q.device, stream, name, qp, qt, qh, HQ, lay.num_kv_heads, lay.head_dim, float(scale),
+        lse.data_ptr(), ctypes.byref(seqs), *(t.data_ptr() for t in cache), ctypes.byref(lay),
+        *wargs, _ptr(err_flag))
+
+
+def attention_weights(q, lse, cu_draft, parents, context_lens, block_table, k_cache, scale,
+                      max_draft, weights, err_flag=None, stream=None):
+    """Add to weights (fp32 [S, Hkv, positions]) what the drafted tokens'
+    attention gave every cached row: += for the context, = for the drafted
+    tokens' own rows.  q, lse: the inputs and the result of tree_attention.
+    Tokens whose parent is <= -2 count nothing."""
+    _attention_weights("sconv_kv_attention_weights", q, lse, cu_draft, parents, context_lens,
+                       block_table, (k_cache,), _cache_pair(k_cache, None), scale, max_draft,
+                       weights, err_flag, stream)
+
+
+def attention_weights_mxfp8(q, lse, cu_draft, parents, context_lens, block_table, k_data, k_scale,
+                            scale, max_draft, weights, err_flag=None, stream=None):
+    """attention_weights over an MXFP8 cache."""
+    _attention_weights("sconv_kv_attention_weights_mxfp8", q, lse, cu_draft, parents, context_lens,
+                       block_table, (k_data, k_scale),
+                       _mx_layout(k_data, k_scale, k_data, k_scale), scale, max_draft, weights,
+                       err_flag, stream)
+
+
+def _tree_accept(name, k, v, cu_draft, parents, leaves, context_lens, block_table, W, conv_state,
+                 cache, lay, new_lens, weights, state_indices, state_positions, err_flag, stream):
+    kp, rs = _rows(k, "k")
+    vp, rs_v = _rows(v, "v")
+    if rs != rs_v or v.shape != k.shape:
+        raise ValueError("k and v must share shape and row stride")
+    seqs = _paged(context_lens, block_table, cu_draft, parents, k.shape[0], MAX_DRAFT)
+    S = seqs.num_seqs
+    _dense(leaves, "leaves", _I32, (S,))
+    _dense(new_lens, "new_lens", _I32, (S,))
+    if state_indices is not None:
+        _dense(state_indices, "state_indices", _I32, (S,))
+    if state_positions is not None:
+        _dense(state_positions, "state_positions", torch.int64, (S,))
+    C2 = 2 * lay.num_kv_heads * lay.head_dim
+    if W > 1:
+        if conv_state.dtype != _BF16 or conv_state.dim() != 3 or not conv_state.is_contiguous() or \
+                tuple(conv_state.shape[1:]) != (W - 1, C2):
+            raise ValueError(f"conv_state must be contiguous bfloat16 [pool, {W - 1}, {C2}]")
+    wargs = (None, 0, 0, 0)
+    if weights is not None:
+        wargs = _weight_rows(weights, "weights", S, lay.num_kv_heads)
+    _same_device(k.device, v=v, cu_draft=cu_draft, parents=parents, leaves=leaves,
+                 context_lens=context_lens, block_table=block_table, cache=cache[0],
+                 conv_state=conv_state, new_lens=new_lens, weights=weights)
+    _on(k.device, stream, name, kp, vp, rs, ctypes.byref(seqs), leaves.data_ptr(), int(W),
+        lay.num_kv_heads, lay.head_dim, _ptr(conv_state) if W > 1 else None, _ptr(state_indices),
+        conv_state.shape[0] if W > 1 else 0, _ptr(state_positions),
+        *(t.data_ptr() for t in cache), ctypes.byref(lay), *wargs, new_lens.data_ptr(),
+        _ptr(err_flag))
+
+
+def tree_accept(k, v, cu_draft, parents, leaves, context_lens, block_table, W, conv_state, k_cache,
+                v_cache, new_lens, weights=None, state_indices=None, state_positions=None,
+                err_flag=None, stream=None):
+    """Accept the path that ends at draft leaves[i] (int32 [S], local index; -1:
+    none) of every sequence: its cache rows (and weights, if given) move to
+    the positions behind the context, conv_state takes its raw rows, and
+    new_lens (int32 [S], not context_lens itself) gets the new lengths.  k,
+    v: the raw rows that tree_step was given."""
+    _tree_accept("sconv_kv_tree_accept", k, v, cu_draft, parents, leaves, context_lens, block_table,
+                 W, conv_state, (k_cache, v_cache), _cache_pair(k_cache, v_cache), new_lens,
+                 weights, state_indices, state_positions, err_flag, stream)
+
+
+def tree_accept_mxfp8(k, v, cu_draft, parents, leaves, context_lens, block_table, W, conv_state,
+                      k_data, k_scale, v_data, v_scale, new_lens, weights=None,
+                      state_indices=None, state_positions=None, err_flag=None, stream=None):
+    """tree_accept over an MXFP8 cache."""
+    _tree_accept("sconv_kv_tree_accept_mxfp8", k, v, cu_draft, parents, leaves, context_lens,
+                 block_table, W, conv_state, (k_data, k_scale, v_data, v_scale),
+                 _mx_layout(k_data, k_scale, v_data, v_scale), new_lens, weights, state_indices,
+                 state_positions, err_flag, stream)
+
+
+def _evict(name, weights, context_lens, block_table, cache, lay, sinks, recent, kept, new_lens,
+           weights_out, err_flag, stream):
+    seqs = _paged(context_lens, block_table)
+    S, H = seqs.num_seqs, lay.num_kv_heads
+    keep = kept.shape[-1]
+    _dense(kept, "kept", _I32, (S, H, keep))
+    _dense(new_lens, "new_lens", _I32, (S,))
+    wargs = _weight_rows(weights, "weights", S, H)
+    oargs = (None, 0, 0, 0)
+    if weights_out is not None:
+        oargs = _weight_rows(weights_out, "weights_out", S, H)
+    _same_device(weights.device, context_lens=context_lens, block_table=block_table,
+                 cache=cache[0], kept=kept, new_lens=new_lens, weights_out=weights_out)
+    _on(weights.device, stream, name, *wargs, ctypes.byref(seqs), keep, int(sinks), int(recent), H,
+        lay.head_dim, *(t.data_ptr() for t in cache), ctypes.byref(lay), kept.data_ptr(),
+        new_lens.data_ptr(), *oargs, _ptr(err_flag))
+
+
+def evict(weights, context_lens, block_table, k_cache, v_cache, sinks, recent, kept, new_lens,
+          weights_out=None, err_flag=None, stream=None):
+    """Keep kept.shape[2] rows of every longer sequence, per K/V head: the
+    first `sinks`, the last `recent` and those of the largest weight (fp32
+    [S, Hkv, positions]; ties to the lower position).  They move to the front in
+    their order; kept (int32 [S, Hkv, keep]) gets their old positions (-1
+    behind a shorter sequence), new_lens the lengths, weights_out (not
+    weights itself) their weights."""
+    _evict("sconv_kv_evict", weights, context_lens, block_table, (k_cache, v_cache),
+           _cache_pair(k_cache, v_cache), sinks, recent, kept, new_lens, weights_out, err_flag,
+           stream)
+
+
+def evict_mxfp8(weights, context_lens, block_table, k_data, k_scale, v_data, v_scale, sinks,
+                recent, kept, new_lens, weights_out=None, err_flag=None, stream=None):
+    """evict over an MXFP8 cache."""
+    _evict("sconv_kv_evict_mxfp8", weights, context_lens, block_table,
+           (k_data, k_scale, v_data, v_scale), _mx_layout(k_data, k_scale, v_data, v_scale), sinks,
+           recent, kept, new_lens, weights_out, err_flag, stream)
