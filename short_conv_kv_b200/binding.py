@@ -51,6 +51,8 @@ class Paged(ctypes.Structure):
 class SconvKVError(RuntimeError):
     def __init__(self, code, where):
         msg = _lib.sconv_kv_strerror(code).decode()
+        if code == ERR_SCRATCH and "tree_attention" in where:
+            msg = "the workspace is too small (see tree_attention_workspace)"
         if code == ERR_CUDA:
             msg += ": " + _lib.sconv_kv_last_cuda_error().decode()
         super().__init__(f"{where} failed with status {code}: {msg}")

@@ -1,8 +1,8 @@
 """Build the C-ABI library ``libsconvkv.so`` (sm_100a) in-tree with nvcc.
 
-The host code (``csrc/sconv_kv.cu``, ``csrc/tree_ops.cu``) and the kernel-instance translation
-units (``csrc/inst_*.cu``) are compiled to objects in parallel, then linked
-into one shared library.
+The host code (``csrc/tree_ops.cu``, which includes ``csrc/sconv_kv.cu``) and
+the kernel-instance translation units (``csrc/inst_*.cu``) are compiled to
+objects in parallel, then linked into one shared library.
 """
 import concurrent.futures
 import os
@@ -14,7 +14,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libsconvkv.so")
-SOURCES = [os.path.join(CSRC, "sconv_kv.cu"), os.path.join(CSRC, "tree_ops.cu")] + sorted(
+# tree_ops.cu includes sconv_kv.cu
+SOURCES = [os.path.join(CSRC, "tree_ops.cu")] + sorted(
     os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.startswith("inst_") and f.endswith(".cu"))
 DEPS = [os.path.join(CSRC, f) for f in os.listdir(CSRC)] + [
     os.path.join(INCLUDE, f) for f in os.listdir(INCLUDE)]

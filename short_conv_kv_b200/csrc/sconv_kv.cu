@@ -9,7 +9,6 @@
 
 #include "sconv_kv.h"
 #include "common.cuh"
-#include "host.h"
 #include "instances.h"
 #include "stages.cuh"
 
@@ -639,33 +638,9 @@ int launch_stage_state(sconv::StageParams* P, void* stream) {
 
 }  // namespace
 
-namespace sconv {
-
-int host_step_params(const void* k, const void* v, int64_t row_stride, const void* conv_w_k,
-                     const void* conv_w_v, const float* gamma_k, const float* gamma_v, int W,
-                     int num_kv_heads, int head_dim, void* conv_state, int64_t state_pool_size,
-                     const int64_t* slot_mapping, void* k_cache, void* v_cache,
-                     const sconv_kv_cache_layout_t* layout, uint8_t* k_scale, uint8_t* v_scale,
-                     bool mx, const sconv_kv_options_t* options, StepParams* P) {
-  const int rc = validate_common(k, v, row_stride, conv_w_k, conv_w_v, gamma_k, gamma_v, W,
-                                 num_kv_heads, head_dim, conv_state, state_pool_size,
-                                 slot_mapping, k_cache, v_cache, layout, P, k_scale, v_scale, mx);
-  return rc != SCONV_KV_OK ? rc : apply_options(options, head_dim, P);
-}
-int host_launch(const void* fn, dim3 grid, dim3 block, void** args, size_t smem, void* stream) {
-  return launch(fn, grid, block, args, smem, stream);
-}
-bool host_smem(const void* fn, size_t smem) { return smem_attr_set(fn, smem); }
-int host_sm_count() { return sm_count(); }
-int host_resident(const void* fn, int threads, size_t smem, int fallback) {
-  return resident_per_sm(fn, threads, smem, fallback);
-}
-
-}  // namespace sconv
-
 extern "C" {
 
-int sconv_kv_version(void) { return 200; }
+int sconv_kv_version(void) { return 100; }
 
 const char* sconv_kv_strerror(int status) {
   switch (status) {
@@ -675,7 +650,7 @@ const char* sconv_kv_strerror(int status) {
     case SCONV_KV_ERR_ALIGN: return "pointer or stride not 16-byte aligned";
     case SCONV_KV_ERR_UNSUPPORTED: return "unsupported combination";
     case SCONV_KV_ERR_CUDA: return "CUDA error at launch (see sconv_kv_last_cuda_error)";
-    case SCONV_KV_ERR_SCRATCH: return "call needs more scratch (static buffer or workspace) than it has";
+    case SCONV_KV_ERR_SCRATCH: return "call needs more than the static scratch buffer";
     default: return "unknown status";
   }
 }

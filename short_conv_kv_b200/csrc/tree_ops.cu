@@ -1,12 +1,15 @@
 // C ABI of the drafted-tree operators and the eviction: argument checks, launch
 // geometry and dispatch.  See include/sconv_kv.h for the contract.
+//
+// sconv_kv.cu, the entry points of the step itself, is part of this
+// translation unit: both share its helpers (launch, argument checks, the caches
+// of device properties and the text of the last CUDA error).
+#include "sconv_kv.cu"
+
 #include <math.h>
-#include <string.h>
 
 #include <algorithm>
 
-#include "host.h"
-#include "sconv_kv.h"
 #include "tree_instances.h"
 
 namespace {
@@ -129,8 +132,8 @@ int plan_attend(int max_draft, int HQ, int H, int D, bool mx, AttendPlan* A) {
   A->fn = sconv::pick_attend_rows(D, A->nt, mx);
   if (!A->fn) return SCONV_KV_ERR_UNSUPPORTED;
   const void* fn = reinterpret_cast<const void*>(A->fn);
-  if (!sconv::host_smem(fn, A->smem)) return SCONV_KV_ERR_CUDA;
-  A->parts = sconv::host_sm_count() * sconv::host_resident(fn, A->threads, A->smem, 2);
+  if (!smem_attr_set(fn, A->smem)) return SCONV_KV_ERR_CUDA;
+  A->parts = sm_count() * resident_per_sm(fn, A->threads, A->smem, 2);
   return SCONV_KV_OK;
 }
 
@@ -187,7 +190,7 @@ int attention_impl(const void* q, int64_t q_tok, int64_t q_head, int HQ, int H, 
   P.parts = A.parts;
   {
     void* args[] = {&P};
-    rc = sconv::host_launch(reinterpret_cast<const void*>(A.fn), dim3(A.parts), dim3(A.threads),
+    rc = launch(reinterpret_cast<const void*>(A.fn), dim3(A.parts), dim3(A.threads),
                             args, A.smem, stream);
     if (rc != SCONV_KV_OK) return rc;
   }
@@ -195,7 +198,7 @@ int attention_impl(const void* q, int64_t q_tok, int64_t q_head, int HQ, int H, 
   const int64_t x = static_cast<int64_t>(seqs->num_seqs) * mtiles;
   if (x > INT32_MAX) return SCONV_KV_ERR_SHAPE;
   void* args[] = {&P, &A.rows, &A.tile, &mtiles};
-  return sconv::host_launch(reinterpret_cast<const void*>(sconv::pick_attend_join(D)),
+  return launch(reinterpret_cast<const void*>(sconv::pick_attend_join(D)),
                             dim3(static_cast<unsigned>(x), H, (A.rows + 3) / 4), dim3(128), args,
                             0, stream);
 }
@@ -236,10 +239,10 @@ int weights_impl(const void* q, int64_t q_tok, int64_t q_head, int HQ, int H, in
   const size_t smem = sconv::weigh_smem(D);
   const int threads = 32 * sconv::kWeighWarps;
   const void* f = reinterpret_cast<const void*>(fn);
-  if (!sconv::host_smem(f, smem)) return SCONV_KV_ERR_CUDA;
-  const int ctas = sconv::host_sm_count() * sconv::host_resident(f, threads, smem, 2);
+  if (!smem_attr_set(f, smem)) return SCONV_KV_ERR_CUDA;
+  const int ctas = sm_count() * resident_per_sm(f, threads, smem, 2);
   void* args[] = {&W};
-  return sconv::host_launch(f, dim3(ctas), dim3(threads), args, smem, stream);
+  return launch(f, dim3(ctas), dim3(threads), args, smem, stream);
 }
 
 int step_impl(const void* k, const void* v, int64_t row_stride, int64_t num_tokens,
@@ -253,9 +256,9 @@ int step_impl(const void* k, const void* v, int64_t row_stride, int64_t num_toke
   if (num_seqs == 0 || num_tokens == 0) return SCONV_KV_OK;
   TreeStepParams A;
   memset(&A, 0, sizeof A);
-  const int rc = sconv::host_step_params(k, v, row_stride, wk, wv, gk, gv, W, H, D,
-                                         const_cast<void*>(state), pool, slots, kc, vc, layout, ks,
-                                         vs, mx, options, &A.s);
+  int rc = validate_common(k, v, row_stride, wk, wv, gk, gv, W, H, D, const_cast<void*>(state),
+                           pool, slots, kc, vc, layout, &A.s, ks, vs, mx);
+  if (rc == SCONV_KV_OK) rc = apply_options(options, D, &A.s);
   if (rc != SCONV_KV_OK) return rc;
   if (!cu || !parents) return SCONV_KV_ERR_NULL;
   A.s.num_tokens = num_tokens;
@@ -265,14 +268,14 @@ int step_impl(const void* k, const void* v, int64_t row_stride, int64_t num_toke
   A.s.state_indices = state_indices;
   A.s.err = err;
   A.parents = parents;
-  const bool lv = options && (options->gamma_head_stride != 0 || options->state_positions);
+  const bool lv = uses_layout_variants(options);
   const sconv::TreeStepFn fn = sconv::pick_tree_step(W, D, mx, lv);
   if (!fn) return SCONV_KV_ERR_UNSUPPORTED;
   const int64_t blocks = (num_tokens * A.s.NG + 255) / 256;
   const unsigned grid =
-      static_cast<unsigned>(std::min<int64_t>(blocks, 16ll * sconv::host_sm_count()));
+      static_cast<unsigned>(std::min<int64_t>(blocks, 16ll * sm_count()));
   void* args[] = {&A};
-  return sconv::host_launch(reinterpret_cast<const void*>(fn), dim3(grid), dim3(256), args, 0,
+  return launch(reinterpret_cast<const void*>(fn), dim3(grid), dim3(256), args, 0,
                             stream);
 }
 
@@ -324,11 +327,11 @@ int accept_impl(const void* k, const void* v, int64_t row_stride, const sconv_kv
   A.state_pos = state_positions;
   // enough slices for one vector a thread, fewer when the sequences fill the GPU
   const int64_t vecs = static_cast<int64_t>(H) * D / 8;
-  const int64_t fill = (8ll * sconv::host_sm_count() + seqs->num_seqs - 1) / seqs->num_seqs;
+  const int64_t fill = (8ll * sm_count() + seqs->num_seqs - 1) / seqs->num_seqs;
   const unsigned slices = static_cast<unsigned>(
       std::max<int64_t>(1, std::min<int64_t>({(vecs + 255) / 256, fill, 64})));
   void* args[] = {&A};
-  return sconv::host_launch(reinterpret_cast<const void*>(sconv::accept_fn()),
+  return launch(reinterpret_cast<const void*>(sconv::accept_fn()),
                             dim3(static_cast<unsigned>(seqs->num_seqs), slices), dim3(256), args, 0,
                             stream);
 }
@@ -372,10 +375,10 @@ int evict_impl(const float* weights, int64_t positions, int64_t w_seq, int64_t w
   A.kept = kept;
   A.new_lens = new_lens;
   void* args[] = {&A};
-  rc = sconv::host_launch(reinterpret_cast<const void*>(sconv::evict_select_fn()),
+  rc = launch(reinterpret_cast<const void*>(sconv::evict_select_fn()),
                           dim3(H, seqs->num_seqs), dim3(sconv::kSelectThreads), args, 0, stream);
   if (rc != SCONV_KV_OK) return rc;
-  return sconv::host_launch(reinterpret_cast<const void*>(sconv::evict_move_fn()),
+  return launch(reinterpret_cast<const void*>(sconv::evict_move_fn()),
                             dim3(mx ? 4 : 2, H, seqs->num_seqs), dim3(sconv::kMoveThreads), args, 0,
                             stream);
 }
