@@ -92,12 +92,13 @@ __device__ __forceinline__ int warp_seq_of(const int32_t* cu, int S, int64_t t) 
 
 // Ancestor masks of a sequence's drafted tokens in shared memory, by pointer
 // doubling: anc[j] = bits of j and its ancestors, 0 for an unused token.
-// All `nthreads` threads of the block take part (barriers inside); needs
-// nthreads >= kMaxDraft.  A parent at or behind its own token, or an unused
+// Threads 0 .. n-1 (n >= kMaxDraft) of the block take part; `meet` is a barrier
+// among them.  A parent at or behind its own token, or an unused
 // one, makes the token unused and raises the tree flag.
+template <class Meet>
 __device__ __forceinline__ void ancestor_masks(const PagedSeqs& Q, const SeqView& s,
-                                               uint32_t (*anc)[kMaskWords], int* ptr,
-                                               bool report) {
+                                               uint32_t (*anc)[kMaskWords], int* ptr, bool report,
+                                               Meet meet) {
   const int j = threadIdx.x;
   const bool mine = j < s.n;
   uint32_t m[kMaskWords];
@@ -118,7 +119,7 @@ __device__ __forceinline__ void ancestor_masks(const PagedSeqs& Q, const SeqView
     for (int w = 0; w < kMaskWords; ++w) anc[j][w] = m[w];
   }
   const bool unused = p == -2;
-  __syncthreads();
+  meet();
   for (int reach = 1; reach < s.n; reach <<= 1) {
     int np = p;
     if (mine && p >= 0) {
@@ -126,21 +127,26 @@ __device__ __forceinline__ void ancestor_masks(const PagedSeqs& Q, const SeqView
 #pragma unroll
       for (int w = 0; w < kMaskWords; ++w) m[w] |= anc[p][w];
     }
-    __syncthreads();
+    meet();
     if (mine && p >= 0) {
       p = np;
       ptr[j] = p;
 #pragma unroll
       for (int w = 0; w < kMaskWords; ++w) anc[j][w] = m[w];
     }
-    __syncthreads();
+    meet();
   }
   if (mine && p == -2) {
 #pragma unroll
     for (int w = 0; w < kMaskWords; ++w) anc[j][w] = 0;
     if (report && (bad || !unused)) raise_flag(Q.err, kFlagTree);
   }
-  __syncthreads();
+  meet();
+}
+__device__ __forceinline__ void ancestor_masks(const PagedSeqs& Q, const SeqView& s,
+                                               uint32_t (*anc)[kMaskWords], int* ptr,
+                                               bool report) {  // the whole block
+  ancestor_masks(Q, s, anc, ptr, report, [] { __syncthreads(); });
 }
 
 }  // namespace sconv

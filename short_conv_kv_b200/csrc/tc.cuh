@@ -1,0 +1,411 @@
+// Fifth-generation tensor cores (sm_100a): tensor memory, matrix
+// instructions, descriptors, and the producer that feeds them with rows of
+// the paged cache.
+#pragma once
+#include "attend.cuh"
+
+namespace sconv {
+
+constexpr uint64_t kTcTimeoutNs = 1000000000ull;
+
+// ------------------------------------------------------------ tensor memory
+
+__device__ __forceinline__ void tmem_alloc(uint32_t* to, uint32_t cols) {  // one warp
+  asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                   smem_u32(to)),
+               "r"(cols)
+               : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+}
+__device__ __forceinline__ void tmem_free(uint32_t at, uint32_t cols) {  // the same warp
+  asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(at), "r"(cols));
+}
+__device__ __forceinline__ void tc_fence_before() {
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ void tc_fence_after() {
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_wait_ld() {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+// 32 columns of this warp's 32 lanes: thread l gets lane l.
+__device__ __forceinline__ void tmem_ld32(float (&r)[32], uint32_t at) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]),
+        "=f"(r[7]), "=f"(r[8]), "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]),
+        "=f"(r[14]), "=f"(r[15]), "=f"(r[16]), "=f"(r[17]), "=f"(r[18]), "=f"(r[19]),
+        "=f"(r[20]), "=f"(r[21]), "=f"(r[22]), "=f"(r[23]), "=f"(r[24]), "=f"(r[25]),
+        "=f"(r[26]), "=f"(r[27]), "=f"(r[28]), "=f"(r[29]), "=f"(r[30]), "=f"(r[31])
+      : "r"(at));
+}
+// The registers of a load are only defined behind tmem_wait_ld(); this ties
+// their uses to it.
+__device__ __forceinline__ void tmem_landed(float (&r)[32]) {
+  tmem_wait_ld();
+#pragma unroll
+  for (int i = 0; i < 32; ++i) asm volatile("" : "+f"(r[i]));
+}
+__device__ __forceinline__ void tmem_st16(uint32_t at, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(at),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
+      "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t at, const float (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(at),
+      "f"(r[0]), "f"(r[1]), "f"(r[2]), "f"(r[3]), "f"(r[4]), "f"(r[5]), "f"(r[6]), "f"(r[7]),
+      "f"(r[8]), "f"(r[9]), "f"(r[10]), "f"(r[11]), "f"(r[12]), "f"(r[13]), "f"(r[14]),
+      "f"(r[15]), "f"(r[16]), "f"(r[17]), "f"(r[18]), "f"(r[19]), "f"(r[20]), "f"(r[21]),
+      "f"(r[22]), "f"(r[23]), "f"(r[24]), "f"(r[25]), "f"(r[26]), "f"(r[27]), "f"(r[28]),
+      "f"(r[29]), "f"(r[30]), "f"(r[31])
+      : "memory");
+}
+
+// --------------------------------------------------------- matrix products
+
+// Shared-memory operand in 128-byte swizzled atoms (8 rows of 128 bytes, 16-byte
+// chunk c of row r at chunk c ^ (r & 7)), atoms 1024 bytes apart along the
+// rows; `lead` is the distance of the next 64 columns where the columns are the
+// product's M or N dimension (unused where they are its K dimension).
+__device__ __forceinline__ uint64_t tc_desc(uint32_t addr, uint32_t lead) {
+  return static_cast<uint64_t>((addr & 0x3ffffu) >> 4) |
+         (static_cast<uint64_t>((lead & 0x3ffffu) >> 4) << 16) |
+         (static_cast<uint64_t>(1024 >> 4) << 32) | (1ull << 46) | (2ull << 61);
+}
+// bf16 x bf16 -> fp32, M rows, N columns; b_rows: B's rows are its K dimension.
+__host__ __device__ constexpr uint32_t tc_idesc(int M, int N, bool b_rows) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | (b_rows ? 1u << 16 : 0u) |
+         (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
+}
+__device__ __forceinline__ void tc_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                       bool accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(accumulate))
+      : "memory");
+}
+__device__ __forceinline__ void tc_mma_tmem(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+                                            bool accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(accumulate))
+      : "memory");
+}
+// Arrive on `bar` when the products issued so far by this thread are complete.
+__device__ __forceinline__ void tc_commit(uint64_t* bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+                   smem_u32(bar))
+               : "memory");
+}
+
+// --------------------------------------------------------- async copies
+
+// 16 bytes (or 16 zero bytes) to shared memory.
+__device__ __forceinline__ void cp16(uint32_t to, const void* from, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from),
+               "r"(there ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void cp4(uint32_t to, const void* from, bool there) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(to), "l"(from),
+               "r"(there ? 4 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void cp_wait_n(int n) {  // all but the last n groups
+  if (n <= 0) cp_wait<0>();
+  else if (n == 1) cp_wait<1>();
+  else if (n == 2) cp_wait<2>();
+  else if (n == 3) cp_wait<3>();
+  else if (n == 4) cp_wait<4>();
+  else cp_wait<5>();
+}
+__device__ __forceinline__ void async_proxy_fence() {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+__device__ __forceinline__ uint4 lds16(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(a)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t lds4(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ void sts16(uint32_t a, const uint4& v) {
+  asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z),
+               "r"(v.w)
+               : "memory");
+}
+
+// Four E4M3 codes to bf16 pairs as e4m3x4_bf16, by one multiplication: `both` is
+// 2^120 times the scale, which needs a scale byte of 134 (2^7) at most.
+// NaN codes come out finite: the caller looks for them.
+__device__ __forceinline__ void e4m3x4_bf16_fast(uint32_t w, uint32_t both, uint32_t& lo,
+                                                 uint32_t& hi) {
+  const uint32_t a = __byte_perm(w, 0, 0x1404);
+  const uint32_t b = __byte_perm(w, 0, 0x3424);
+  lo = bf16x2_mul((a & 0x80008000u) | ((a >> 4) & 0x07f007f0u), both);
+  hi = bf16x2_mul((b & 0x80008000u) | ((b >> 4) & 0x07f007f0u), both);
+}
+// Whether any of a word's codes is NaN (0x7f, 0xff): bits 7 of the result.
+__device__ __forceinline__ uint32_t e4m3_nan(uint32_t w) {
+  return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+}
+
+// ------------------------------------------------------------ the producer
+//
+// A unit is a tile of KEYS cache rows of one K/V head, K's or V's, as bf16 in swizzled
+// shared memory: [D / 64][KEYS][64], each block of 64 columns in 128-byte
+// atoms.  Rows come through the block table, so they are gathered 16 bytes a
+// copy (any page size, any strides); a warp brings KEYS / kWarps whole
+// rows, whose offsets its lanes looked up.
+//
+// bf16: copies land in place, and a thread signals a unit when its own pieces
+// have landed; kLag units are in flight while the ring has room, and what is
+// pending is signalled at once when it has none.
+// MXFP8: a thread copies its pieces of the codes and, as an aligned word each,
+// their scale bytes into a small ring of its own, kDepth units ahead, and
+// writes them to the unit as bf16 (exact).  No thread reads another's pieces.
+
+struct FeedRing {
+  uint32_t units;  // shared-memory address of the first unit
+  uint32_t raw;    // MXFP8: this thread's pieces
+  uint64_t* full;
+  uint64_t* empty;
+  volatile int* abort;
+  int count;  // units in the ring
+};
+
+template <int D, int KEYS, bool MX>
+struct Feed {
+  static constexpr int kWarps = MX ? 8 : 4;
+  static constexpr int kThreads = 32 * kWarps;
+  static constexpr int kUnit = KEYS * D * 2;
+  static constexpr int kKeysWarp = KEYS / kWarps;          // rows of a warp
+  static constexpr int kChunks = MX ? D / 16 : D / 8;      // pieces of a row
+  static constexpr int kRowsStep = 32 / kChunks;           // rows a warp takes a step
+  static constexpr int kPieces = kKeysWarp / kRowsStep;    // pieces of a thread
+  static constexpr int kDepth = 3;
+  static constexpr int kRawUnit = MX ? kPieces * kThreads * 20 : 0;
+  static constexpr int kRawBytes = kDepth * kRawUnit;
+  static_assert(kKeysWarp % kRowsStep == 0 && kPieces <= 16, "");
+
+  FeedRing R;
+  int lane, warp, tid;
+  int slot = 0, phase = 0;   // the next unit to issue (bf16) or to write (MXFP8)
+  bool wrapped = false;
+  int sig = 0, pend = 0;     // bf16: the next unit to signal; issued, not signalled
+  int stage = 0;             // MXFP8: the raw stage of the next unit
+  uint32_t where[kDepth];    // MXFP8: which byte of its word a scale is, 2 bits a piece
+  int rel[kDepth];           // MXFP8: rows from here on are cleaned
+  bool ok = true, found = false;
+
+  __device__ __forceinline__ void init(const FeedRing& ring, int t) {
+    R = ring;
+    tid = t;
+    lane = t & 31;
+    warp = t >> 5;
+#pragma unroll
+    for (int i = 0; i < kDepth; ++i) {
+      where[i] = 0;
+      rel[i] = KEYS;
+    }
+  }
+  __device__ __forceinline__ int my_key() const { return warp * kKeysWarp + lane % kKeysWarp; }
+  __device__ __forceinline__ void bump(int& s) const { s = s + 1 == R.count ? 0 : s + 1; }
+  __device__ __forceinline__ void wait_empty() {
+    if (ok && !mbar_wait(R.empty + slot, phase, R.abort, kTcTimeoutNs)) ok = false;
+  }
+  __device__ __forceinline__ void advance() {
+    bump(slot);
+    if (slot == 0) {
+      if (wrapped) phase ^= 1;
+      wrapped = true;
+    }
+  }
+  __device__ __forceinline__ int row_of(int i) const {
+    return warp * kKeysWarp + i * kRowsStep + lane / kChunks;
+  }
+  __device__ __forceinline__ uint32_t place(int unit, int key, int chunk) const {
+    return R.units + unit * kUnit + (chunk >> 3) * (KEYS * 128) + key * 128 +
+           (((chunk & 7) ^ (key & 7)) << 4);
+  }
+  __device__ __forceinline__ uint32_t off_of(uint32_t off8, int i) const {
+    return __shfl_sync(kFullMask, off8, i * kRowsStep + lane / kChunks);
+  }
+
+  // ---- bf16
+  __device__ __forceinline__ void signal() {
+    cp_wait_n(pend - 1);
+    async_proxy_fence();
+    mbar_arrive(R.full + sig);
+    bump(sig);
+    --pend;
+  }
+  // One unit: off8 is the offset (in units of 8 elements) of the row of my_key(), ~0u
+  // for a row of zeros; rows at or behind `clean` lose NaN and infinities.
+  __device__ __forceinline__ void bring_bf16(const uint8_t* base, uint32_t off8, int clean) {
+    if (wrapped && ok && !mbar_try_wait(R.empty + slot, phase)) {
+      while (pend) signal();
+      wait_empty();
+    }
+    const int chunk = lane % kChunks;
+    const uint8_t* col = base + chunk * 16;
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) {
+      const uint32_t o = off_of(off8, i);
+      if (ok) cp16(place(slot, row_of(i), chunk),
+                   col + (o == ~0u ? 0 : static_cast<uint64_t>(o) * 16), o != ~0u);
+    }
+    cp_commit();
+    ++pend;
+    if (clean < KEYS) {
+      while (pend > 1) signal();
+      cp_wait<0>();
+#pragma unroll 1
+      for (int i = 0; i < kPieces; ++i)
+        if (row_of(i) >= clean) {
+          const uint32_t a = place(slot, row_of(i), chunk);
+          bool bad = false;
+          const uint4 v = clean16<false>(lds16(a), bad);
+          if (bad) {
+            sts16(a, v);
+            found = true;
+          }
+        }
+      // whoever reads the result learns of it through the unit's barrier
+      if (found) *(R.abort + 1) = 1;
+      signal();
+    }
+    advance();
+    if (pend > R.count - 2) signal();
+  }
+
+  // ---- MXFP8
+  __device__ __forceinline__ uint32_t raw_at(int st, int i) const {
+    return R.raw + st * kRawUnit + i * (kThreads * 16);
+  }
+  __device__ __forceinline__ uint32_t scale_at(int st, int i) const {
+    return R.raw - tid * 16 + st * kRawUnit + kPieces * kThreads * 16 + i * (kThreads * 4) + tid * 4;
+  }
+  __device__ __forceinline__ void write_unit(int st, uint32_t bytes, int clean) {
+    if (wrapped) wait_empty();
+    if (ok) {
+#pragma unroll
+      for (int i = 0; i < kPieces; ++i) {
+        const uint4 w = lds16(raw_at(st, i));
+        const uint32_t sb = (lds4(scale_at(st, i)) >> (8 * ((bytes >> (2 * i)) & 3u))) & 255u;
+        uint4 a, b;
+        const uint32_t nan = e4m3_nan(w.x) | e4m3_nan(w.y) | e4m3_nan(w.z) | e4m3_nan(w.w);
+        if (nan == 0 && sb <= 134u) {
+          const uint32_t both = ((sb + 120u) << 7) * 0x10001u;
+          e4m3x4_bf16_fast(w.x, both, a.x, a.y);
+          e4m3x4_bf16_fast(w.y, both, a.z, a.w);
+          e4m3x4_bf16_fast(w.z, both, b.x, b.y);
+          e4m3x4_bf16_fast(w.w, both, b.z, b.w);
+        } else {
+          const uint32_t sc = e8m0_bf16x2(sb);
+          e4m3x4_bf16(w.x, sc, a.x, a.y);
+          e4m3x4_bf16(w.y, sc, a.z, a.w);
+          e4m3x4_bf16(w.z, sc, b.x, b.y);
+          e4m3x4_bf16(w.w, sc, b.z, b.w);
+          if (row_of(i) >= clean) {
+            bool bad = false;
+            a = clean16<false>(a, bad);
+            b = clean16<false>(b, bad);
+            if (bad) *(R.abort + 1) = 1;
+          }
+        }
+        const int chunk = (lane % kChunks) * 2;
+        sts16(place(slot, row_of(i), chunk), a);
+        sts16(place(slot, row_of(i), chunk + 1), b);
+      }
+    }
+    async_proxy_fence();
+    mbar_arrive(R.full + slot);
+    advance();
+  }
+  __device__ __forceinline__ void bring_mx(const uint8_t* base, const uint8_t* scales,
+                                           uint32_t off8, int clean) {
+    const int chunk = lane % kChunks;
+    uint32_t bytes = 0;
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) {
+      const uint32_t o = off_of(off8, i);
+      const uint64_t o8 = o == ~0u ? 0 : o;
+      const uint8_t* sp = scales + (o8 >> 2) + (chunk >> 1);
+      const uint32_t lowbits = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(sp)) & 3u;
+      if (ok) {
+        cp16(raw_at(stage, i), base + o8 * 8 + chunk * 16, o != ~0u);
+        cp4(scale_at(stage, i), sp - lowbits, o != ~0u);
+      }
+      bytes |= lowbits << (2 * i);
+    }
+    cp_commit();
+#pragma unroll
+    for (int i = kDepth - 1; i > 0; --i) {
+      where[i] = where[i - 1];
+      rel[i] = rel[i - 1];
+    }
+    where[0] = bytes;
+    rel[0] = clean;
+    ++pend;
+    stage = stage + 1 == kDepth ? 0 : stage + 1;
+    if (pend == kDepth) {
+      cp_wait<kDepth - 1>();
+      write_unit(stage, where[kDepth - 1], rel[kDepth - 1]);
+      --pend;
+    }
+  }
+
+  __device__ __forceinline__ void bring(const uint8_t* base, const uint8_t* scales, uint32_t off8,
+                                        int clean) {
+    if constexpr (MX) bring_mx(base, scales, off8, clean);
+    else bring_bf16(base, off8, clean);
+  }
+  // Everything still under way.
+  __device__ __forceinline__ void finish() {
+    if constexpr (MX) {
+      static_assert(kDepth == 3, "");
+      cp_wait<0>();
+      // pend <= 2: the oldest first
+      if (pend == 2) {
+        write_unit(stage == 2 ? 0 : stage + 1, where[1], rel[1]);
+        pend = 1;
+      }
+      if (pend == 1) {
+        write_unit(stage == 0 ? kDepth - 1 : stage - 1, where[0], rel[0]);
+        pend = 0;
+      }
+    } else {
+      while (pend) signal();
+      cp_wait<0>();
+    }
+  }
+};
+
+}  // namespace sconv

@@ -1,5 +1,5 @@
 // Kernel instances of the drafted-tree entry points, picked at run time
-// (inst_tree_step.cu, inst_attend.cu, inst_evict.cu).
+// (inst_tree_step.cu, inst_attend.cu, inst_attend_tc.cu, inst_evict.cu).
 #pragma once
 #include "tree_params.h"
 
@@ -8,11 +8,23 @@ namespace sconv {
 using TreeStepFn = void (*)(TreeStepParams);
 using AttendFn = void (*)(AttendParams);
 using JoinFn = void (*)(AttendParams, int, int, int);
+using AttendTcFn = void (*)(AttendParams, int, int);
 using WeighFn = void (*)(WeighParams);
 
 // nullptr for an unsupported combination.
 TreeStepFn pick_tree_step(int W, int D, bool mx, bool lv);
 AttendFn pick_attend_rows(int D, int nt, bool mx);
+// attend_tc_kernel for up to `rows` query rows a K/V head: its threads, rows a unit,
+// keys a tile, units in the ring and dynamic shared memory.
+struct AttendTc {
+  AttendTcFn fn;
+  int threads;
+  int rows;
+  int tile;
+  int units;
+  size_t smem;
+};
+AttendTc pick_attend_tc(int D, bool mx, int rows);
 JoinFn pick_attend_join(int D);
 WeighFn pick_weigh(int D, bool mx);
 void (*accept_fn())(AcceptParams);

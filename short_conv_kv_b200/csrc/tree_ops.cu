@@ -111,10 +111,12 @@ int check_heads(int HQ, int H, int64_t tok, int64_t head, int D) {
 }
 
 // How a call's attention is laid out: rows an M-tile, keys a tile, and the
-// CTAs that share the tiles.
+// CTAs that share the tiles.  Up to 16 rows a K/V head (8 with D = 256, whose
+// accumulators would not fit) go to attend_rows_kernel, more to
+// attend_tc_kernel.
 struct AttendPlan {
-  sconv::AttendFn fn;
-  int nt;
+  const void* fn;
+  int units;  // of attend_tc_kernel's ring; 0: attend_rows_kernel
   int rows;
   int tile;
   int threads;
@@ -124,16 +126,26 @@ struct AttendPlan {
 
 int plan_attend(int max_draft, int HQ, int H, int D, bool mx, AttendPlan* A) {
   const int rows = max_draft * (HQ / H);
-  A->nt = D == 256 || rows <= 8 ? 1 : 2;
-  A->rows = 8 * A->nt;
-  A->tile = sconv::kRowsTile;
-  A->threads = 32 * sconv::kRowsWarps;
-  A->smem = sconv::attend_rows_smem(D, A->nt);
-  A->fn = sconv::pick_attend_rows(D, A->nt, mx);
-  if (!A->fn) return SCONV_KV_ERR_UNSUPPORTED;
-  const void* fn = reinterpret_cast<const void*>(A->fn);
-  if (!smem_attr_set(fn, A->smem)) return SCONV_KV_ERR_CUDA;
-  A->parts = sm_count() * resident_per_sm(fn, A->threads, A->smem, 2);
+  if (rows <= (D == 256 ? 8 : 16)) {
+    const int nt = rows <= 8 ? 1 : 2;
+    A->units = 0;
+    A->rows = 8 * nt;
+    A->tile = sconv::kRowsTile;
+    A->threads = 32 * sconv::kRowsWarps;
+    A->smem = sconv::attend_rows_smem(D, nt);
+    A->fn = reinterpret_cast<const void*>(sconv::pick_attend_rows(D, nt, mx));
+    if (!A->fn) return SCONV_KV_ERR_UNSUPPORTED;
+  } else {
+    const sconv::AttendTc t = sconv::pick_attend_tc(D, mx, rows);
+    A->units = t.units;
+    A->rows = t.rows;
+    A->tile = t.tile;
+    A->threads = t.threads;
+    A->smem = t.smem;
+    A->fn = reinterpret_cast<const void*>(t.fn);
+  }
+  if (!smem_attr_set(A->fn, A->smem)) return SCONV_KV_ERR_CUDA;
+  A->parts = sm_count() * (A->units ? 1 : resident_per_sm(A->fn, A->threads, A->smem, 2));
   return SCONV_KV_OK;
 }
 
@@ -189,9 +201,8 @@ int attention_impl(const void* q, int64_t q_tok, int64_t q_head, int HQ, int H, 
   P.part_o = reinterpret_cast<float*>(w);
   P.parts = A.parts;
   {
-    void* args[] = {&P};
-    rc = launch(reinterpret_cast<const void*>(A.fn), dim3(A.parts), dim3(A.threads),
-                            args, A.smem, stream);
+    void* args[] = {&P, &A.rows, &A.units};  // attend_rows_kernel takes the first
+    rc = launch(A.fn, dim3(A.parts), dim3(A.threads), args, A.smem, stream);
     if (rc != SCONV_KV_OK) return rc;
   }
   int mtiles = (seqs->max_draft * P.g + A.rows - 1) / A.rows;
