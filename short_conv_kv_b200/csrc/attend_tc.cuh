@@ -26,9 +26,21 @@ struct TcShape {
   static constexpr int kSoftWarps = 4 * kStreams;
   static constexpr uint32_t kOut = D == 256 ? 2 * kKeys : 256;  // first column of O
 };
+// Softmax warpgroups, producers, and a warpgroup of which one warp issues the
+// products.  Two softmax warpgroups get more registers than an even share:
+// with 16 warps of 128 launched, 2 * 184 + 2 * 72 = 4 * 128; with 20 warps
+// of 96 (MXFP8), 2 * 144 + 2 * 72 + 48 = 5 * 96.
 template <int D, bool MX>
 __host__ __device__ constexpr int tc_threads() {
-  return 32 * (TcShape<D>::kSoftWarps + Feed<D, TcShape<D>::kKeys, MX>::kWarps + 1);
+  return 32 * (TcShape<D>::kSoftWarps + Feed<D, TcShape<D>::kKeys, MX>::kWarps + 4);
+}
+template <int N>
+__device__ __forceinline__ void more_registers() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void fewer_registers() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
 // Bits a0 .. a0+31 of the row's view of the keys behind the context: a < 0
@@ -119,10 +131,12 @@ __global__ void __launch_bounds__(tc_threads<D, MX>(), 1)
 
   if (warp < T::kSoftWarps) {
     // ------------------------------------------------------------- softmax
+    if constexpr (NS == 2) more_registers<MX ? 144 : 184>();
     const int stream = warp >> 2;
     const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // this warp's lanes
     const int r = (warp & 3) * 32 + lane;                          // row of the stream's tile
-    const float scale = fabsf(P.scale_log2);
+    // (0 would make NaN of a masked -inf; 2^-100 of any sane score is 0 as well)
+    const float scale = fmaxf(fabsf(P.scale_log2), 0x1p-100f);
     const uint32_t flip = P.scale_log2 < 0.f ? 0x80008000u : 0u;  // the sign goes to Q
     uint32_t seen_scores[2] = {0, 0}, seen_outs[2] = {0, 0};
     int segment = 0, masked_seq = -1;
@@ -168,29 +182,60 @@ __global__ void __launch_bounds__(tc_threads<D, MX>(), 1)
           const uint32_t at = tmem + lanes + b * TN;
           const int a0 = (t0 + t) * TN - sv.ctx;
           const bool tail = a0 + TN > 0;
-          float x[32];
-          float m = -INFINITY;
-#pragma unroll
-          for (int c = 0; c < TN / 32; ++c) {
-            tmem_ld32(x, at + c * 32);
-            tmem_landed(x);
-            if (tail) {
-              const uint32_t vis = seen32(s_anc[tok], a0 + c * 32, used);
+          if (tail) {  // masked scores become -inf where they lie
+            float x[32];
+#pragma unroll 1
+            for (int c = 0; c < TN; c += 32) {
+              if (a0 + c + 32 <= 0) continue;
+              const uint32_t vis = seen32(s_anc[tok], a0 + c, used);
+              tmem_ld32(x, at + c);
+              tmem_landed(x);
 #pragma unroll
               for (int e = 0; e < 32; ++e) x[e] = (vis >> e) & 1u ? x[e] : -INFINITY;
+              tmem_st32(at + c, x);
             }
-            float m0 = x[0], m1 = x[1];
-#pragma unroll
-            for (int e = 2; e < 32; e += 4) {
-              m0 = fmaxf(m0, fmaxf(x[e], x[e + 1]));
-              if (e + 2 < 32) m1 = fmaxf(m1, fmaxf(x[e + 2], x[e + 3]));
-            }
-            m = fmaxf(m, fmaxf(m0, m1));
+            tmem_wait_st();
           }
-          m = m == -INFINITY ? m : m * scale;
-          const bool grow = m > mx + 8.f;  // true at the first finite score
-          if (__any_sync(kFullMask, grow)) {
-            const float to = grow ? m : mx;
+          // One pass with the maximum so far.  A tile whose own maximum is
+          // more than 2^8 above it (a row's first tile among them) is done again with that:
+          // the probabilities are stored behind the pass, so S is still there.
+          uint32_t p[TN / 32][16];
+          float2 acc;
+#pragma unroll 1
+          for (int pass = 0; pass < 3; ++pass) {
+            const float base = mx == -INFINITY ? 0.f : mx;
+            const float2 sc = make_float2(scale, scale), nb = make_float2(-base, -base);
+            acc = make_float2(0.f, 0.f);
+            float m0 = -INFINITY, m1 = -INFINITY;
+            float x[2][32];
+            tmem_ld32(x[0], at);
+#pragma unroll
+            for (int c = 0; c < TN / 32; ++c) {
+              tmem_landed(x[c & 1]);
+              if (c + 1 < TN / 32) tmem_ld32(x[(c + 1) & 1], at + (c + 1) * 32);
+#pragma unroll
+              for (int e = 0; e < 32; e += 4) {
+                float2 y = ffma2(make_float2(x[c & 1][e], x[c & 1][e + 1]), sc, nb);
+                float2 z = ffma2(make_float2(x[c & 1][e + 2], x[c & 1][e + 3]), sc, nb);
+                m0 = fmaxf(m0, fmaxf(y.x, y.y));
+                m1 = fmaxf(m1, fmaxf(z.x, z.y));
+                y.x = ex2(y.x);
+                y.y = ex2(y.y);
+                z.x = ex2(z.x);
+                z.y = ex2(z.y);
+                acc = __fadd2_rn(acc, __fadd2_rn(y, z));
+                p[c][e / 2] = pack_bf16x2(y);
+                p[c][e / 2 + 1] = pack_bf16x2(z);
+                // (done here and now: postponed, twice the numbers would be live)
+                asm volatile(""
+                             : "+r"(p[c][e / 2]), "+r"(p[c][e / 2 + 1]), "+f"(acc.x), "+f"(acc.y),
+                               "+f"(m0), "+f"(m1));
+              }
+            }
+            const float top = fmaxf(m0, m1);
+            const bool grow = top > (mx == -INFINITY ? -INFINITY : 8.f);
+            if (!__any_sync(kFullMask, grow)) break;
+            const float to = grow ? base + top : mx;
             const float w = merge_weight(mx, to);
             mx = to;
             sum *= w;
@@ -200,42 +245,20 @@ __global__ void __launch_bounds__(tc_threads<D, MX>(), 1)
               if (NS == 1) wait(&s_out[(t - 1) & 1], seen_outs[(t - 1) & 1] + ((t - 1) >> 1));
               tc_fence_after();
               const uint32_t o = tmem + lanes + T::kOut + (NS == 1 ? 0 : stream) * D;
-              if (ok) {
+              if (!ok) break;
 #pragma unroll 1
-                for (int c = 0; c < D; c += 32) {
-                  tmem_ld32(x, o + c);
-                  tmem_landed(x);
+              for (int c = 0; c < D; c += 32) {
+                tmem_ld32(x[0], o + c);
+                tmem_landed(x[0]);
 #pragma unroll
-                  for (int e = 0; e < 32; ++e) x[e] *= w;
-                  tmem_st32(o + c, x);
-                }
+                for (int e = 0; e < 32; ++e) x[0][e] *= w;
+                tmem_st32(o + c, x[0]);
               }
             }
           }
-          const float base = mx == -INFINITY ? 0.f : mx;
-          const float2 sc = make_float2(scale, scale), nb = make_float2(-base, -base);
-          float2 acc = make_float2(0.f, 0.f);
 #pragma unroll
-          for (int c = 0; c < TN / 32; ++c) {
-            tmem_ld32(x, at + c * 32);
-            tmem_landed(x);
-            uint32_t vis = ~0u;
-            if (tail) vis = seen32(s_anc[tok], a0 + c * 32, used);
-            uint32_t p[16];
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              float2 y = ffma2(make_float2(x[2 * e], x[2 * e + 1]), sc, nb);
-              if (tail) {
-                y.x = (vis >> (2 * e)) & 1u ? y.x : -INFINITY;
-                y.y = (vis >> (2 * e + 1)) & 1u ? y.y : -INFINITY;
-              }
-              y.x = ex2(y.x);
-              y.y = ex2(y.y);
-              acc = __fadd2_rn(acc, y);
-              p[e] = pack_bf16x2(y);
-            }
-            tmem_st16(at + c * 16, p);
-          }
+          for (int c = 0; c < TN / 32; ++c)
+            tmem_st16(at + c * 16, p[c]);
           sum += acc.x + acc.y;
           tmem_wait_st();
         }
@@ -276,8 +299,6 @@ __global__ void __launch_bounds__(tc_threads<D, MX>(), 1)
         const uint32_t o = tmem + lanes + T::kOut + (pair ? stream * D : 0);
         const float inv = !whole ? 1.f : sum == 0.f ? 0.f : 1.f / sum;
         const bool none = !used;
-        const int key1 = min(total, (t0 + tiles) * TN);
-        const bool bad = *reinterpret_cast<volatile int*>(&s_abort[1]);
 #pragma unroll 1
         for (int d = d0; d < d1; d += 32) {
           float x[32];
@@ -296,10 +317,6 @@ __global__ void __launch_bounds__(tc_threads<D, MX>(), 1)
             }
           }
           if (mine < rows) {
-            if (bad)
-              for (int e = 0; e < 32; ++e)
-                x[e] = restore_nonfinite<MX>(P, seq, sv.ctx, sv.n, h, s_anc[tok], t0 * TN, key1,
-                                             d + e, x[e]);
             if (whole) {
               uint16_t* to = P.out + (sv.a + tok) * P.o_tok + hq * P.o_head + d;
 #pragma unroll
@@ -322,6 +339,19 @@ __global__ void __launch_bounds__(tc_threads<D, MX>(), 1)
             }
           }
         }
+        if (*reinterpret_cast<volatile int*>(&s_abort[1]) && used)  // rare
+          for (int d = d0; d < d1; ++d) {
+            const float v = restore_nonfinite<MX>(P, seq, sv.ctx, sv.n, h, s_anc[tok], t0 * TN,
+                                                  min(total, (t0 + tiles) * TN), d, 0.f);
+            if (fabsf(v) < INFINITY) continue;
+            if (whole) {
+              uint16_t* to = P.out + (sv.a + tok) * P.o_tok + hq * P.o_head + d;
+              const float o = __uint_as_float(static_cast<uint32_t>(*to) << 16);
+              *to = static_cast<uint16_t>(pack_bf16x2(make_float2(o + v, 0.f)));
+            } else {
+              P.part_o[(slot * rows_unit + mine) * D + d] += v;
+            }
+          }
         if (mine < rows && d0 == 0) {
           const float l = none ? 0.f : sum;
           if (!whole)
@@ -338,6 +368,7 @@ __global__ void __launch_bounds__(tc_threads<D, MX>(), 1)
     if (!ok && lane == 0) raise_flag(P.s.err, kFlagTimeout);
   } else if (warp < T::kSoftWarps + F::kWarps) {
     // ------------------------------------------------------------ producers
+    if constexpr (NS == 2) fewer_registers<72>();
     F feed;
     {
       FeedRing R;
@@ -349,42 +380,57 @@ __global__ void __launch_bounds__(tc_threads<D, MX>(), 1)
       R.count = ring_units;
       feed.init(R, tid - kSoft);
     }
-    while (cur < end) {
-      locate();
-      const int64_t head = h * P.s.stride_head;
-      const uint8_t* kb = P.c.k + head * (MX ? 1 : 2);
-      const uint8_t* vb = P.c.v + head * (MX ? 1 : 2);
-      const uint8_t* ksb = MX ? P.c.ks + (head >> 5) : nullptr;
-      const uint8_t* vsb = MX ? P.c.vs + (head >> 5) : nullptr;
-      const int32_t* table = P.s.table + seq * P.s.table_stride;
-      const int key0 = t0 * TN + feed.my_key();
-      auto page_at = [&](int t) { return __ldg(table + page_index(P.s, min(key0 + t * TN, total - 1))); };
-      auto off_at = [&](int t, int page) -> uint32_t {
-        const int p = key0 + t * TN;
-        if (p >= total) return ~0u;
-        if (static_cast<unsigned>(page) >= static_cast<unsigned>(P.s.num_pages)) {
-          raise_flag(P.s.err, kFlagSlotRange);
-          page = 0;
+    // One unit a round; order in a segment (see the products): K0 V0 K1 V1 .. for a
+    // pair, K0 K1 V0 K2 V1 .. otherwise.
+    const uint8_t *kb = nullptr, *vb = nullptr, *ksb = nullptr, *vsb = nullptr;
+    const int32_t* table = nullptr;
+    int key0 = 0, u = 0, page = 0;
+    uint32_t off0 = ~0u, off1 = ~0u;  // of the tiles of either parity
+    tiles = 0;
+    while (true) {
+      const bool have = u < 2 * tiles || cur < end;
+      int t = 0, clean = TN;
+      bool is_v = false;
+      if (have) {
+        if (u == 2 * tiles) {  // the next segment
+          locate();
+          const int64_t head = h * P.s.stride_head;
+          kb = P.c.k + head * (MX ? 1 : 2);
+          vb = P.c.v + head * (MX ? 1 : 2);
+          ksb = MX ? P.c.ks + (head >> 5) : nullptr;
+          vsb = MX ? P.c.vs + (head >> 5) : nullptr;
+          table = P.s.table + seq * P.s.table_stride;
+          key0 = t0 * TN + feed.my_key();
+          page = __ldg(table + page_index(P.s, min(key0, total - 1)));
+          cur += tiles;
+          u = 0;
         }
-        return static_cast<uint32_t>(row_offset(P.s, page, p) >> 3);
-      };
-      auto clean_from = [&](int t) { return max(0, min(TN, sv.ctx - (t0 + t) * TN)); };
-      uint32_t off0 = off_at(0, page_at(0));
-      int page = page_at(1);
-      feed.bring(kb, ksb, off0, TN);
-      for (int t = 0; t < tiles; ++t) {
-        const uint32_t off1 = off_at(t + 1, page);
-        page = page_at(t + 2);
-        if (!pair && t + 1 < tiles) feed.bring(kb, ksb, off1, TN);
-        feed.bring(vb, vsb, off0, clean_from(t));
-        if (pair && t + 1 < tiles) feed.bring(kb, ksb, off1, TN);
-        off0 = off1;
+        const int w = !pair && u == 2 * tiles - 1 ? u + 1 : u;
+        is_v = pair ? w & 1 : w > 0 && !(w & 1);
+        t = pair ? w >> 1 : is_v ? (w >> 1) - 1 : (w + 1) >> 1;
+        if (is_v) {
+          clean = max(0, min(TN, sv.ctx - (t0 + t) * TN));
+        } else {
+          const int p = key0 + t * TN;
+          if (static_cast<unsigned>(page) >= static_cast<unsigned>(P.s.num_pages)) {
+            if (p < total) raise_flag(P.s.err, kFlagSlotRange);
+            page = 0;
+          }
+          const uint32_t o =
+              p < total ? static_cast<uint32_t>(row_offset(P.s, page, p) >> 3) : ~0u;
+          if (t & 1) off1 = o;
+          else off0 = o;
+          page = __ldg(table + page_index(P.s, min(p + TN, total - 1)));  // of the next tile
+        }
+        ++u;
       }
-      cur += tiles;
+      if (!feed.bring(have, is_v ? vb : kb, is_v ? vsb : ksb, t & 1 ? off1 : off0, clean))
+        break;
     }
-    feed.finish();
-  } else if (lane == 0) {
+  } else {
     // ------------------------------------------------------------- products
+    if constexpr (NS == 2) fewer_registers<MX ? 48 : 72>();
+    if (warp == T::kSoftWarps + F::kWarps && lane == 0) {
     constexpr uint32_t kIdS = tc_idesc(128, TN, false), kIdO = tc_idesc(128, D, true);
     constexpr uint32_t kBlock = TN * 128;  // 64 columns of a unit
     uint32_t probs[2] = {0, 0}, queries = 0;
@@ -393,6 +439,11 @@ __global__ void __launch_bounds__(tc_threads<D, MX>(), 1)
     bool ok = true;
     auto wait = [&](uint64_t* bar, uint32_t count) {
       if (ok) ok = mbar_wait(bar, count & 1u, s_abort, kTcTimeoutNs);
+    };
+    auto unit = [&](int at, uint32_t par) {  // until the unit is there
+      wait(&s_full[at], par);
+      async_proxy_fence();
+      tc_fence_after();
     };
     auto next = [&] {
       if (++slot == ring_units) {
@@ -426,8 +477,7 @@ __global__ void __launch_bounds__(tc_threads<D, MX>(), 1)
       locate();
       wait(&s_query, queries++);
       if (pair) {
-        wait(&s_full[slot], phase);
-        tc_fence_after();
+        unit(slot, phase);
         score(0, 0);
         score(1, 1);
         free_unit();
@@ -444,13 +494,13 @@ __global__ void __launch_bounds__(tc_threads<D, MX>(), 1)
           for (int s = 0; s < 2; ++s) {
             wait(&s_prob[s], probs[s]++);
             slot = v_slot;
-            if (s == 0) wait(&s_full[v_slot], v_phase);
+            if (s == 0) unit(v_slot, v_phase);
             tc_fence_after();
             output(s, s, t == 0);
             if (s == 1 && ok) tc_commit(&s_empty[v_slot]);
             if (more) {
               slot = k_slot;
-              if (s == 0) wait(&s_full[k_slot], k_phase);
+              if (s == 0) unit(k_slot, k_phase);
               tc_fence_after();
               score(s, s);
               if (s == 1 && ok) tc_commit(&s_empty[k_slot]);
@@ -463,21 +513,18 @@ __global__ void __launch_bounds__(tc_threads<D, MX>(), 1)
         }
       } else {
         for (int t = 0; t < 2 && t < tiles; ++t) {
-          wait(&s_full[slot], phase);
-          tc_fence_after();
+          unit(slot, phase);
           score(t, 0);
           free_unit();
         }
         for (int t = 0; t < tiles && ok; ++t) {
           const int b = t & 1;
           wait(&s_prob[b], probs[b]++);
-          wait(&s_full[slot], phase);
-          tc_fence_after();
+          unit(slot, phase);
           output(b, NS == 2 ? b : 0, t < NS);
           free_unit();
           if (t + 2 < tiles) {
-            wait(&s_full[slot], phase);
-            tc_fence_after();
+            unit(slot, phase);
             score(b, 0);
             free_unit();
           }
@@ -490,6 +537,7 @@ __global__ void __launch_bounds__(tc_threads<D, MX>(), 1)
     int dummy[1] = {0};
     if (!mbar_wait(&s_drain, 0, dummy, kDrainTimeoutNs)) ok = false;
     if (!ok) raise_flag(P.s.err, kFlagTimeout);
+    }
   }
   __syncthreads();
   tc_fence_after();

@@ -131,13 +131,9 @@ template <int N>
 __device__ __forceinline__ void cp_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
-__device__ __forceinline__ void cp_wait_n(int n) {  // all but the last n groups
-  if (n <= 0) cp_wait<0>();
-  else if (n == 1) cp_wait<1>();
-  else if (n == 2) cp_wait<2>();
-  else if (n == 3) cp_wait<3>();
-  else if (n == 4) cp_wait<4>();
-  else cp_wait<5>();
+// One of `bar`'s arrivals, made when this thread's copies so far have landed.
+__device__ __forceinline__ void cp_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 __device__ __forceinline__ void async_proxy_fence() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -176,6 +172,25 @@ __device__ __forceinline__ uint32_t e4m3_nan(uint32_t w) {
   return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
 }
 
+// Sixteen codes with any scale byte, NaN codes among them (rare).  With `clean`, NaN
+// and infinities become 0; returns whether there were any.
+__device__ __noinline__ bool e4m3x16_slow(uint4 w, uint32_t sb, bool clean, uint4* out) {
+  const uint32_t sc = e8m0_bf16x2(sb);
+  uint4 a, b;
+  e4m3x4_bf16(w.x, sc, a.x, a.y);
+  e4m3x4_bf16(w.y, sc, a.z, a.w);
+  e4m3x4_bf16(w.z, sc, b.x, b.y);
+  e4m3x4_bf16(w.w, sc, b.z, b.w);
+  bool bad = false;
+  if (clean) {
+    a = clean16<false>(a, bad);
+    b = clean16<false>(b, bad);
+  }
+  out[0] = a;
+  out[1] = b;
+  return bad;
+}
+
 // ------------------------------------------------------------ the producer
 //
 // A unit is a tile of KEYS cache rows of one K/V head, K's or V's, as bf16 in swizzled
@@ -184,20 +199,23 @@ __device__ __forceinline__ uint32_t e4m3_nan(uint32_t w) {
 // copy (any page size, any strides); a warp brings KEYS / kWarps whole
 // rows, whose offsets its lanes looked up.
 //
-// bf16: copies land in place, and a thread signals a unit when its own pieces
-// have landed; kLag units are in flight while the ring has room, and what is
-// pending is signalled at once when it has none.
+// bf16: copies land in place and arrive on the unit's barrier by themselves, so
+// the ring is in flight but for the units in use.  (The thread that
+// issues the products fences the proxies behind its wait.)
 // MXFP8: a thread copies its pieces of the codes and, as an aligned word each,
 // their scale bytes into a small ring of its own, kDepth units ahead, and
 // writes them to the unit as bf16 (exact).  No thread reads another's pieces.
+//
+// One call site brings all units: several copies of this code, with the
+// softmax's, fall out of the instruction cache.
 
 struct FeedRing {
   uint32_t units;  // shared-memory address of the first unit
   uint32_t raw;    // MXFP8: this thread's pieces
   uint64_t* full;
   uint64_t* empty;
-  volatile int* abort;
-  int count;  // units in the ring
+  volatile int* abort;  // [1]: a V row was cleaned
+  int count;            // units in the ring
 };
 
 template <int D, int KEYS, bool MX>
@@ -216,13 +234,12 @@ struct Feed {
 
   FeedRing R;
   int lane, warp, tid;
-  int slot = 0, phase = 0;   // the next unit to issue (bf16) or to write (MXFP8)
+  int slot = 0, phase = 0;  // the unit to fill next
   bool wrapped = false;
-  int sig = 0, pend = 0;     // bf16: the next unit to signal; issued, not signalled
-  int stage = 0;             // MXFP8: the raw stage of the next unit
-  uint32_t where[kDepth];    // MXFP8: which byte of its word a scale is, 2 bits a piece
-  int rel[kDepth];           // MXFP8: rows from here on are cleaned
-  bool ok = true, found = false;
+  int pend = 0, stage = 0;  // MXFP8: units copied but not written; the raw stage of the next
+  uint32_t where[kDepth];   // MXFP8: which byte of its word a scale is, 2 bits a piece
+  int rel[kDepth];          // MXFP8: rows from here on are cleaned
+  bool ok = true;
 
   __device__ __forceinline__ void init(const FeedRing& ring, int t) {
     R = ring;
@@ -236,13 +253,12 @@ struct Feed {
     }
   }
   __device__ __forceinline__ int my_key() const { return warp * kKeysWarp + lane % kKeysWarp; }
-  __device__ __forceinline__ void bump(int& s) const { s = s + 1 == R.count ? 0 : s + 1; }
   __device__ __forceinline__ void wait_empty() {
-    if (ok && !mbar_wait(R.empty + slot, phase, R.abort, kTcTimeoutNs)) ok = false;
+    if (wrapped && ok && !mbar_wait(R.empty + slot, phase, R.abort, kTcTimeoutNs)) ok = false;
   }
   __device__ __forceinline__ void advance() {
-    bump(slot);
-    if (slot == 0) {
+    if (++slot == R.count) {
+      slot = 0;
       if (wrapped) phase ^= 1;
       wrapped = true;
     }
@@ -250,62 +266,46 @@ struct Feed {
   __device__ __forceinline__ int row_of(int i) const {
     return warp * kKeysWarp + i * kRowsStep + lane / kChunks;
   }
-  __device__ __forceinline__ uint32_t place(int unit, int key, int chunk) const {
-    return R.units + unit * kUnit + (chunk >> 3) * (KEYS * 128) + key * 128 +
+  __device__ __forceinline__ uint32_t place(int key, int chunk) const {
+    return R.units + slot * kUnit + (chunk >> 3) * (KEYS * 128) + key * 128 +
            (((chunk & 7) ^ (key & 7)) << 4);
   }
   __device__ __forceinline__ uint32_t off_of(uint32_t off8, int i) const {
     return __shfl_sync(kFullMask, off8, i * kRowsStep + lane / kChunks);
   }
 
-  // ---- bf16
-  __device__ __forceinline__ void signal() {
-    cp_wait_n(pend - 1);
-    async_proxy_fence();
-    mbar_arrive(R.full + sig);
-    bump(sig);
-    --pend;
-  }
-  // One unit: off8 is the offset (in units of 8 elements) of the row of my_key(), ~0u
-  // for a row of zeros; rows at or behind `clean` lose NaN and infinities.
   __device__ __forceinline__ void bring_bf16(const uint8_t* base, uint32_t off8, int clean) {
-    if (wrapped && ok && !mbar_try_wait(R.empty + slot, phase)) {
-      while (pend) signal();
-      wait_empty();
-    }
+    wait_empty();
     const int chunk = lane % kChunks;
     const uint8_t* col = base + chunk * 16;
 #pragma unroll
     for (int i = 0; i < kPieces; ++i) {
       const uint32_t o = off_of(off8, i);
-      if (ok) cp16(place(slot, row_of(i), chunk),
+      if (ok) cp16(place(row_of(i), chunk),
                    col + (o == ~0u ? 0 : static_cast<uint64_t>(o) * 16), o != ~0u);
     }
-    cp_commit();
-    ++pend;
-    if (clean < KEYS) {
-      while (pend > 1) signal();
+    if (clean >= KEYS) {
+      cp_arrive(R.full + slot);
+    } else {
+      cp_commit();
       cp_wait<0>();
 #pragma unroll 1
       for (int i = 0; i < kPieces; ++i)
         if (row_of(i) >= clean) {
-          const uint32_t a = place(slot, row_of(i), chunk);
+          const uint32_t a = place(row_of(i), chunk);
           bool bad = false;
           const uint4 v = clean16<false>(lds16(a), bad);
           if (bad) {
             sts16(a, v);
-            found = true;
+            R.abort[1] = 1;
           }
         }
-      // whoever reads the result learns of it through the unit's barrier
-      if (found) *(R.abort + 1) = 1;
-      signal();
+      async_proxy_fence();
+      mbar_arrive(R.full + slot);
     }
     advance();
-    if (pend > R.count - 2) signal();
   }
 
-  // ---- MXFP8
   __device__ __forceinline__ uint32_t raw_at(int st, int i) const {
     return R.raw + st * kRawUnit + i * (kThreads * 16);
   }
@@ -313,9 +313,13 @@ struct Feed {
     return R.raw - tid * 16 + st * kRawUnit + kPieces * kThreads * 16 + i * (kThreads * 4) + tid * 4;
   }
   __device__ __forceinline__ void write_unit(int st, uint32_t bytes, int clean) {
-    if (wrapped) wait_empty();
+    wait_empty();
     if (ok) {
-#pragma unroll
+      const int chunk = (lane % kChunks) * 2;
+      // eight neighbours of a row would write two blocks' same banks: half of
+      // them begin with their second chunk
+      const int turn = (lane >> 2) & 1;
+#pragma unroll 2
       for (int i = 0; i < kPieces; ++i) {
         const uint4 w = lds16(raw_at(st, i));
         const uint32_t sb = (lds4(scale_at(st, i)) >> (8 * ((bytes >> (2 * i)) & 3u))) & 255u;
@@ -328,82 +332,71 @@ struct Feed {
           e4m3x4_bf16_fast(w.z, both, b.x, b.y);
           e4m3x4_bf16_fast(w.w, both, b.z, b.w);
         } else {
-          const uint32_t sc = e8m0_bf16x2(sb);
-          e4m3x4_bf16(w.x, sc, a.x, a.y);
-          e4m3x4_bf16(w.y, sc, a.z, a.w);
-          e4m3x4_bf16(w.z, sc, b.x, b.y);
-          e4m3x4_bf16(w.w, sc, b.z, b.w);
-          if (row_of(i) >= clean) {
-            bool bad = false;
-            a = clean16<false>(a, bad);
-            b = clean16<false>(b, bad);
-            if (bad) *(R.abort + 1) = 1;
-          }
+          uint4 x[2];
+          if (e4m3x16_slow(w, sb, row_of(i) >= clean, x)) R.abort[1] = 1;
+          a = x[0];
+          b = x[1];
         }
-        const int chunk = (lane % kChunks) * 2;
-        sts16(place(slot, row_of(i), chunk), a);
-        sts16(place(slot, row_of(i), chunk + 1), b);
+        const uint32_t to_a = place(row_of(i), chunk), to_b = place(row_of(i), chunk + 1);
+        sts16(turn ? to_b : to_a, turn ? b : a);
+        sts16(turn ? to_a : to_b, turn ? a : b);
       }
     }
     async_proxy_fence();
     mbar_arrive(R.full + slot);
     advance();
   }
-  __device__ __forceinline__ void bring_mx(const uint8_t* base, const uint8_t* scales,
+  __device__ __forceinline__ void bring_mx(bool have, const uint8_t* base, const uint8_t* scales,
                                            uint32_t off8, int clean) {
-    const int chunk = lane % kChunks;
-    uint32_t bytes = 0;
+    if (have) {
+      const int chunk = lane % kChunks;
+      uint32_t bytes = 0;
 #pragma unroll
-    for (int i = 0; i < kPieces; ++i) {
-      const uint32_t o = off_of(off8, i);
-      const uint64_t o8 = o == ~0u ? 0 : o;
-      const uint8_t* sp = scales + (o8 >> 2) + (chunk >> 1);
-      const uint32_t lowbits = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(sp)) & 3u;
-      if (ok) {
-        cp16(raw_at(stage, i), base + o8 * 8 + chunk * 16, o != ~0u);
-        cp4(scale_at(stage, i), sp - lowbits, o != ~0u);
+      for (int i = 0; i < kPieces; ++i) {
+        const uint32_t o = off_of(off8, i);
+        const uint64_t o8 = o == ~0u ? 0 : o;
+        const uint8_t* sp = scales + (o8 >> 2) + (chunk >> 1);
+        const uint32_t lowbits = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(sp)) & 3u;
+        if (ok) {
+          cp16(raw_at(stage, i), base + o8 * 8 + chunk * 16, o != ~0u);
+          cp4(scale_at(stage, i), sp - lowbits, o != ~0u);
+        }
+        bytes |= lowbits << (2 * i);
       }
-      bytes |= lowbits << (2 * i);
+      where[0] = bytes;
+      rel[0] = clean;
+      ++pend;
     }
+    // an empty group too, so that the oldest unit is always kDepth - 1 groups back
     cp_commit();
+    stage = stage + 1 == kDepth ? 0 : stage + 1;
+    if (pend == kDepth || (!have && pend)) {
+      cp_wait<kDepth - 1>();
+      write_unit(stage, where[kDepth - 1], rel[kDepth - 1]);
+      --pend;
+    }
 #pragma unroll
     for (int i = kDepth - 1; i > 0; --i) {
       where[i] = where[i - 1];
       rel[i] = rel[i - 1];
     }
-    where[0] = bytes;
-    rel[0] = clean;
-    ++pend;
-    stage = stage + 1 == kDepth ? 0 : stage + 1;
-    if (pend == kDepth) {
-      cp_wait<kDepth - 1>();
-      write_unit(stage, where[kDepth - 1], rel[kDepth - 1]);
-      --pend;
-    }
   }
 
-  __device__ __forceinline__ void bring(const uint8_t* base, const uint8_t* scales, uint32_t off8,
-                                        int clean) {
-    if constexpr (MX) bring_mx(base, scales, off8, clean);
-    else bring_bf16(base, off8, clean);
-  }
-  // Everything still under way.
-  __device__ __forceinline__ void finish() {
+  // One unit (with `have`): off8 is the offset, in units of 8 elements, of the row
+  // of my_key(), ~0u for a row of zeros; rows at or behind `clean` lose NaN and
+  // infinities.  Without: go on with what is under way.  False when nothing is.
+  __device__ __forceinline__ bool bring(bool have, const uint8_t* base, const uint8_t* scales,
+                                        uint32_t off8, int clean) {
     if constexpr (MX) {
-      static_assert(kDepth == 3, "");
-      cp_wait<0>();
-      // pend <= 2: the oldest first
-      if (pend == 2) {
-        write_unit(stage == 2 ? 0 : stage + 1, where[1], rel[1]);
-        pend = 1;
-      }
-      if (pend == 1) {
-        write_unit(stage == 0 ? kDepth - 1 : stage - 1, where[0], rel[0]);
-        pend = 0;
-      }
+      bring_mx(have, base, scales, off8, clean);
+      return have || pend > 0;
     } else {
-      while (pend) signal();
-      cp_wait<0>();
+      if (have) bring_bf16(base, off8, clean);
+      else {
+        cp_commit();
+        cp_wait<0>();
+      }
+      return have;
     }
   }
 };
