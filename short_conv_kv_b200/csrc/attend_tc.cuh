@@ -153,17 +153,35 @@ __global__ void __launch_bounds__(tc_threads<D, MX>(), 1)
         masked_seq = seq;
       }
       // ---- Q, rows of both streams
-      for (int x = tid; x < rows * (D / 8); x += kSoft) {
-        const int rr = x / (D / 8), c = x - rr * (D / 8);
-        const int tok = (row0 + rr) / P.g, hg = row0 + rr - tok * P.g;
-        uint4 v = ld_ro(P.q + (sv.a + tok) * P.q_tok + (h * P.g + hg) * P.q_head + c * 8);
-        v.x ^= flip;
-        v.y ^= flip;
-        v.z ^= flip;
-        v.w ^= flip;
-        sts16(smem + (rr >> 7) * kQTile + (c >> 3) * kQBlock + (rr & 127) * 128 +
-                  (((c & 7) ^ (rr & 7)) << 4),
-              v);
+      // (a thread keeps its 8 columns; the loads of eight rows are in flight at once)
+      {
+        constexpr int kStep = kSoft / (D / 8);  // rows apart
+        const int c = tid % (D / 8);
+        const uint16_t* qp = P.q + sv.a * P.q_tok + static_cast<int64_t>(h) * P.g * P.q_head + c * 8;
+        for (int r0 = tid / (D / 8); r0 < rows; r0 += 8 * kStep) {
+          uint4 v[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int rr = r0 + i * kStep;
+            if (rr < rows) {
+              const int tk = (row0 + rr) / P.g;
+              v[i] = ld_ro(qp + tk * P.q_tok + (row0 + rr - tk * P.g) * P.q_head);
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int rr = r0 + i * kStep;
+            if (rr < rows) {
+              v[i].x ^= flip;
+              v[i].y ^= flip;
+              v[i].z ^= flip;
+              v[i].w ^= flip;
+              sts16(smem + (rr >> 7) * kQTile + (c >> 3) * kQBlock + (rr & 127) * 128 +
+                        (((c & 7) ^ (rr & 7)) << 4),
+                    tc_order<MX>(v[i]));
+            }
+          }
+        }
       }
       async_proxy_fence();
       mbar_arrive(&s_query);
@@ -314,6 +332,14 @@ __global__ void __launch_bounds__(tc_threads<D, MX>(), 1)
             } else {
 #pragma unroll
               for (int e = 0; e < 32; ++e) x[e] *= f0;
+            }
+          }
+          if constexpr (MX) {  // back from the units' order of columns
+#pragma unroll
+            for (int e = 0; e < 32; e += 4) {
+              const float y = x[e + 1];
+              x[e + 1] = x[e + 2];
+              x[e + 2] = y;
             }
           }
           if (mine < rows) {

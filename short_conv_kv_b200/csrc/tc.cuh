@@ -157,19 +157,34 @@ __device__ __forceinline__ void sts16(uint32_t a, const uint4& v) {
                : "memory");
 }
 
-// Four E4M3 codes to bf16 pairs as e4m3x4_bf16, by one multiplication: `both` is
-// 2^120 times the scale, which needs a scale byte of 134 (2^7) at most.
-// NaN codes come out finite: the caller looks for them.
-__device__ __forceinline__ void e4m3x4_bf16_fast(uint32_t w, uint32_t both, uint32_t& lo,
-                                                 uint32_t& hi) {
-  const uint32_t a = __byte_perm(w, 0, 0x1404);
-  const uint32_t b = __byte_perm(w, 0, 0x3424);
-  lo = bf16x2_mul((a & 0x80008000u) | ((a >> 4) & 0x07f007f0u), both);
-  hi = bf16x2_mul((b & 0x80008000u) | ((b >> 4) & 0x07f007f0u), both);
+// Four E4M3 codes to bf16 pairs, bytes 0 and 2 to `even`, 1 and 3 to `odd`: the bits
+// as in e4m3x4_bf16, and one multiplication: `both` is 2^120 times the scale, which
+// needs a scale byte of 134 (2^7) at most.  NaN codes (0x7f, 0xff) come out
+// finite; they leave bit 7 of a half of `nan.x`, or bit 11 of one of `nan.y`.
+// The integer pipe bounds this (half the rate of the others), so what can be
+// is a multiply-add: `sixteen` and `one` are registers to keep it so.
+__device__ __forceinline__ void e4m3x4_bf16_fast(uint32_t w, uint32_t both, uint32_t sixteen,
+                                                 uint32_t one, uint32_t& even, uint32_t& odd,
+                                                 uint2& nan) {
+  const uint32_t te = w & 0x007f007fu, to = (w >> 4) & 0x07f007f0u;
+  const uint32_t se = w & 0x00800080u;
+  uint32_t e, ne, no;
+  asm("mad.lo.u32 %0, %1, %2, %3;" : "=r"(e) : "r"(se), "r"(sixteen), "r"(te));
+  asm("mul.lo.u32 %0, %1, %2;" : "=r"(e) : "r"(e), "r"(sixteen));
+  asm("mad.lo.u32 %0, %1, %2, %3;" : "=r"(ne) : "r"(te), "r"(one), "r"(0x00010001u));
+  asm("mad.lo.u32 %0, %1, %2, %3;" : "=r"(no) : "r"(to), "r"(one), "r"(0x00100010u));
+  nan.x |= ne;
+  nan.y |= no;
+  even = bf16x2_mul(e, both);
+  odd = bf16x2_mul((w & 0x80008000u) | to, both);
 }
-// Whether any of a word's codes is NaN (0x7f, 0xff): bits 7 of the result.
-__device__ __forceinline__ uint32_t e4m3_nan(uint32_t w) {
-  return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+// The order in which a decoded unit holds its columns (and Q then too): the
+// middle two of every four are swapped.
+template <bool MX>
+__device__ __forceinline__ uint4 tc_order(const uint4& v) {
+  if constexpr (!MX) return v;
+  return make_uint4(__byte_perm(v.x, v.y, 0x5410), __byte_perm(v.x, v.y, 0x7632),
+                    __byte_perm(v.z, v.w, 0x5410), __byte_perm(v.z, v.w, 0x7632));
 }
 
 // Sixteen codes with any scale byte, NaN codes among them (rare).  With `clean`, NaN
@@ -186,8 +201,8 @@ __device__ __noinline__ bool e4m3x16_slow(uint4 w, uint32_t sb, bool clean, uint
     a = clean16<false>(a, bad);
     b = clean16<false>(b, bad);
   }
-  out[0] = a;
-  out[1] = b;
+  out[0] = tc_order<true>(a);
+  out[1] = tc_order<true>(b);
   return bad;
 }
 
@@ -224,13 +239,17 @@ struct Feed {
   static constexpr int kThreads = 32 * kWarps;
   static constexpr int kUnit = KEYS * D * 2;
   static constexpr int kKeysWarp = KEYS / kWarps;          // rows of a warp
-  static constexpr int kChunks = MX ? D / 16 : D / 8;      // pieces of a row
-  static constexpr int kRowsStep = 32 / kChunks;           // rows a warp takes a step
-  static constexpr int kPieces = kKeysWarp / kRowsStep;    // pieces of a thread
+  // a warp's copy: 4 (MXFP8) or 8 pieces of 16 bytes of 8 or 4 rows, a block of 64
+  // columns; neighbouring rows lie in other banks
+  static constexpr int kCols = MX ? 4 : 8;
+  static constexpr int kRowsStep = 32 / kCols;
+  static constexpr int kBlocks = D / 64;
+  static constexpr int kSteps = kKeysWarp / kRowsStep;
+  static constexpr int kPieces = kSteps * kBlocks;  // of a thread
   static constexpr int kDepth = 3;
   static constexpr int kRawUnit = MX ? kPieces * kThreads * 20 : 0;
   static constexpr int kRawBytes = kDepth * kRawUnit;
-  static_assert(kKeysWarp % kRowsStep == 0 && kPieces <= 16, "");
+  static_assert(kKeysWarp % kRowsStep == 0 && kPieces <= 16, "");  // 2 bits a piece
 
   FeedRing R;
   int lane, warp, tid;
@@ -263,26 +282,27 @@ struct Feed {
       wrapped = true;
     }
   }
-  __device__ __forceinline__ int row_of(int i) const {
-    return warp * kKeysWarp + i * kRowsStep + lane / kChunks;
+  __device__ __forceinline__ int row_of(int i) const {  // of piece i
+    return warp * kKeysWarp + i / kBlocks * kRowsStep + lane / kCols;
   }
-  __device__ __forceinline__ uint32_t place(int key, int chunk) const {
-    return R.units + slot * kUnit + (chunk >> 3) * (KEYS * 128) + key * 128 +
-           (((chunk & 7) ^ (key & 7)) << 4);
-  }
-  __device__ __forceinline__ uint32_t off_of(uint32_t off8, int i) const {
-    return __shfl_sync(kFullMask, off8, i * kRowsStep + lane / kChunks);
+  // where 8 columns go: block i % kBlocks of piece i, chunk of 16 bytes in it
+  __device__ __forceinline__ uint32_t place(int i, int chunk) const {
+    const int key = row_of(i);
+    return R.units + slot * kUnit + i % kBlocks * (KEYS * 128) + key * 128 +
+           ((chunk ^ (key & 7)) << 4);
   }
 
   __device__ __forceinline__ void bring_bf16(const uint8_t* base, uint32_t off8, int clean) {
     wait_empty();
-    const int chunk = lane % kChunks;
+    const int chunk = lane % kCols;
     const uint8_t* col = base + chunk * 16;
 #pragma unroll
-    for (int i = 0; i < kPieces; ++i) {
-      const uint32_t o = off_of(off8, i);
-      if (ok) cp16(place(row_of(i), chunk),
-                   col + (o == ~0u ? 0 : static_cast<uint64_t>(o) * 16), o != ~0u);
+    for (int j = 0; j < kSteps; ++j) {
+      const uint32_t o = __shfl_sync(kFullMask, off8, j * kRowsStep + lane / kCols);
+      const uint8_t* from = col + (o == ~0u ? 0 : static_cast<uint64_t>(o) * 16);
+#pragma unroll
+      for (int b = 0; b < kBlocks; ++b)
+        if (ok) cp16(place(j * kBlocks + b, chunk), from + b * 128, o != ~0u);
     }
     if (clean >= KEYS) {
       cp_arrive(R.full + slot);
@@ -292,7 +312,7 @@ struct Feed {
 #pragma unroll 1
       for (int i = 0; i < kPieces; ++i)
         if (row_of(i) >= clean) {
-          const uint32_t a = place(row_of(i), chunk);
+          const uint32_t a = place(i, chunk);
           bool bad = false;
           const uint4 v = clean16<false>(lds16(a), bad);
           if (bad) {
@@ -315,31 +335,28 @@ struct Feed {
   __device__ __forceinline__ void write_unit(int st, uint32_t bytes, int clean) {
     wait_empty();
     if (ok) {
-      const int chunk = (lane % kChunks) * 2;
-      // eight neighbours of a row would write two blocks' same banks: half of
-      // them begin with their second chunk
-      const int turn = (lane >> 2) & 1;
-#pragma unroll 2
+      const int chunk = (lane % kCols) * 2;
+      uint32_t sixteen = 16u, one = 1u;
+      asm volatile("" : "+r"(sixteen), "+r"(one));
+#pragma unroll kBlocks
       for (int i = 0; i < kPieces; ++i) {
         const uint4 w = lds16(raw_at(st, i));
         const uint32_t sb = (lds4(scale_at(st, i)) >> (8 * ((bytes >> (2 * i)) & 3u))) & 255u;
+        const uint32_t both = (sb + 120u) * 0x00800080u;
         uint4 a, b;
-        const uint32_t nan = e4m3_nan(w.x) | e4m3_nan(w.y) | e4m3_nan(w.z) | e4m3_nan(w.w);
-        if (nan == 0 && sb <= 134u) {
-          const uint32_t both = ((sb + 120u) << 7) * 0x10001u;
-          e4m3x4_bf16_fast(w.x, both, a.x, a.y);
-          e4m3x4_bf16_fast(w.y, both, a.z, a.w);
-          e4m3x4_bf16_fast(w.z, both, b.x, b.y);
-          e4m3x4_bf16_fast(w.w, both, b.z, b.w);
-        } else {
+        uint2 nan = make_uint2(0u, 0u);
+        e4m3x4_bf16_fast(w.x, both, sixteen, one, a.x, a.y, nan);
+        e4m3x4_bf16_fast(w.y, both, sixteen, one, a.z, a.w, nan);
+        e4m3x4_bf16_fast(w.z, both, sixteen, one, b.x, b.y, nan);
+        e4m3x4_bf16_fast(w.w, both, sixteen, one, b.z, b.w, nan);
+        if ((nan.x & 0x00800080u) || (nan.y & 0x08000800u) || sb > 134u) {
           uint4 x[2];
           if (e4m3x16_slow(w, sb, row_of(i) >= clean, x)) R.abort[1] = 1;
           a = x[0];
           b = x[1];
         }
-        const uint32_t to_a = place(row_of(i), chunk), to_b = place(row_of(i), chunk + 1);
-        sts16(turn ? to_b : to_a, turn ? b : a);
-        sts16(turn ? to_a : to_b, turn ? a : b);
+        sts16(place(i, chunk), a);
+        sts16(place(i, chunk + 1), b);
       }
     }
     async_proxy_fence();
@@ -349,19 +366,25 @@ struct Feed {
   __device__ __forceinline__ void bring_mx(bool have, const uint8_t* base, const uint8_t* scales,
                                            uint32_t off8, int clean) {
     if (have) {
-      const int chunk = lane % kChunks;
+      const int chunk = lane % kCols;
       uint32_t bytes = 0;
 #pragma unroll
-      for (int i = 0; i < kPieces; ++i) {
-        const uint32_t o = off_of(off8, i);
+      for (int j = 0; j < kSteps; ++j) {
+        const uint32_t o = __shfl_sync(kFullMask, off8, j * kRowsStep + lane / kCols);
         const uint64_t o8 = o == ~0u ? 0 : o;
+        const uint8_t* from = base + o8 * 8 + chunk * 16;
         const uint8_t* sp = scales + (o8 >> 2) + (chunk >> 1);
-        const uint32_t lowbits = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(sp)) & 3u;
-        if (ok) {
-          cp16(raw_at(stage, i), base + o8 * 8 + chunk * 16, o != ~0u);
-          cp4(scale_at(stage, i), sp - lowbits, o != ~0u);
+#pragma unroll
+        for (int b = 0; b < kBlocks; ++b) {
+          const int i = j * kBlocks + b;
+          const uint32_t low =
+              static_cast<uint32_t>(reinterpret_cast<uintptr_t>(sp + 2 * b)) & 3u;
+          if (ok) {
+            cp16(raw_at(stage, i), from + b * 64, o != ~0u);
+            cp4(scale_at(stage, i), sp + 2 * b - low, o != ~0u);
+          }
+          bytes |= low << (2 * i);
         }
-        bytes |= lowbits << (2 * i);
       }
       where[0] = bytes;
       rel[0] = clean;
