@@ -456,7 +456,9 @@ __global__ void __launch_bounds__(tc_threads<D, MX>(), 1)
   } else {
     // ------------------------------------------------------------- products
     if constexpr (NS == 2) fewer_registers<MX ? 48 : 72>();
-    if (warp == T::kSoftWarps + F::kWarps && lane == 0) {
+    // (the whole warp goes along, so that addresses stay in uniform registers; one
+    // lane issues)
+    if (warp == T::kSoftWarps + F::kWarps) {
     constexpr uint32_t kIdS = tc_idesc(128, TN, false), kIdO = tc_idesc(128, D, true);
     constexpr uint32_t kBlock = TN * 128;  // 64 columns of a unit
     uint32_t probs[2] = {0, 0}, queries = 0;
@@ -465,6 +467,7 @@ __global__ void __launch_bounds__(tc_threads<D, MX>(), 1)
     bool ok = true;
     auto wait = [&](uint64_t* bar, uint32_t count) {
       if (ok) ok = mbar_wait(bar, count & 1u, s_abort, kTcTimeoutNs);
+      ok = __all_sync(kFullMask, ok);
     };
     auto unit = [&](int at, uint32_t par) {  // until the unit is there
       wait(&s_full[at], par);
@@ -477,26 +480,37 @@ __global__ void __launch_bounds__(tc_threads<D, MX>(), 1)
         phase ^= 1;
       }
     };
+    const uint32_t query = tc_desc(smem, 16), keys = tc_desc(units, 16);
+    const uint32_t values = tc_desc(units, kBlock);
+    auto commit = [&](uint64_t* bar) {
+      if (ok && elect_one()) tc_commit(bar);
+      __syncwarp();
+    };
     auto score = [&](int b, int stream) {  // S[b] = Q K^T with the unit in `slot`
-      if (!ok) return;
-      const uint32_t q = smem + stream * kQTile, k = units + slot * F::kUnit;
+      const uint32_t q = query + stream * (kQTile >> 4), k = keys + slot * (F::kUnit >> 4);
+      const uint32_t to = tmem + b * TN;
+      if (ok && elect_one()) {
 #pragma unroll
-      for (int j = 0; j < D / 16; ++j)
-        tc_mma(tmem + b * TN, tc_desc(q + (j >> 2) * kQBlock + (j & 3) * 32, 16),
-               tc_desc(k + (j >> 2) * kBlock + (j & 3) * 32, 16), kIdS, j > 0);
-      tc_commit(&s_score[b]);
+        for (int j = 0; j < D / 16; ++j)
+          tc_mma(to, q + (((j >> 2) * kQBlock + (j & 3) * 32) >> 4),
+                 k + (((j >> 2) * kBlock + (j & 3) * 32) >> 4), kIdS, j > 0);
+        tc_commit(&s_score[b]);
+      }
+      __syncwarp();
     };
     auto output = [&](int b, int stream, bool first) {  // O += P V
-      if (!ok) return;
-      const uint32_t v = units + slot * F::kUnit;
+      const uint32_t v = values + slot * (F::kUnit >> 4);
+      const uint32_t to = tmem + T::kOut + stream * D, p = tmem + b * TN;
+      if (ok && elect_one()) {
+        tc_mma_tmem(to, p, v, kIdO, !first);
 #pragma unroll
-      for (int j = 0; j < TN / 16; ++j)
-        tc_mma_tmem(tmem + T::kOut + stream * D, tmem + b * TN + j * 8,
-                    tc_desc(v + j * 2048, kBlock), kIdO, !first || j > 0);
-      tc_commit(&s_out[b]);
+        for (int j = 1; j < TN / 16; ++j) tc_mma_tmem(to, p + j * 8, v + j * 128, kIdO, 1);
+        tc_commit(&s_out[b]);
+      }
+      __syncwarp();
     };
     auto free_unit = [&] {
-      if (ok) tc_commit(&s_empty[slot]);
+      commit(&s_empty[slot]);
       next();
     };
     while (cur < end && ok) {
@@ -523,13 +537,13 @@ __global__ void __launch_bounds__(tc_threads<D, MX>(), 1)
             if (s == 0) unit(v_slot, v_phase);
             tc_fence_after();
             output(s, s, t == 0);
-            if (s == 1 && ok) tc_commit(&s_empty[v_slot]);
+            if (s == 1) commit(&s_empty[v_slot]);
             if (more) {
               slot = k_slot;
               if (s == 0) unit(k_slot, k_phase);
               tc_fence_after();
               score(s, s);
-              if (s == 1 && ok) tc_commit(&s_empty[k_slot]);
+              if (s == 1) commit(&s_empty[k_slot]);
             }
           }
           slot = v_slot;
@@ -559,10 +573,11 @@ __global__ void __launch_bounds__(tc_threads<D, MX>(), 1)
       cur += tiles;
     }
     // products still under way would write to freed tensor memory
-    tc_commit(&s_drain);
+    if (elect_one()) tc_commit(&s_drain);
+    __syncwarp();
     int dummy[1] = {0};
     if (!mbar_wait(&s_drain, 0, dummy, kDrainTimeoutNs)) ok = false;
-    if (!ok) raise_flag(P.s.err, kFlagTimeout);
+    if (!ok && lane == 0) raise_flag(P.s.err, kFlagTimeout);
     }
   }
   __syncthreads();

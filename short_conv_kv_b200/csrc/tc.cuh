@@ -80,31 +80,42 @@ __device__ __forceinline__ void tmem_st32(uint32_t at, const float (&r)[32]) {
 // chunk c of row r at chunk c ^ (r & 7)), atoms 1024 bytes apart along the
 // rows; `lead` is the distance of the next 64 columns where the columns are the
 // product's M or N dimension (unused where they are its K dimension).
-__device__ __forceinline__ uint64_t tc_desc(uint32_t addr, uint32_t lead) {
-  return static_cast<uint64_t>((addr & 0x3ffffu) >> 4) |
-         (static_cast<uint64_t>((lead & 0x3ffffu) >> 4) << 16) |
-         (static_cast<uint64_t>(1024 >> 4) << 32) | (1ull << 46) | (2ull << 61);
+// The low half holds the address and `lead` (so the operand moves by adding 16-byte
+// units to it), the high half is constant.
+__device__ __forceinline__ uint32_t tc_desc(uint32_t addr, uint32_t lead) {
+  return (addr >> 4) | ((lead >> 4) << 16);
 }
+constexpr uint32_t kDescHigh = (1024u >> 4) | (1u << 14) | (2u << 29);
 // bf16 x bf16 -> fp32, M rows, N columns; b_rows: B's rows are its K dimension.
 __host__ __device__ constexpr uint32_t tc_idesc(int M, int N, bool b_rows) {
   return (1u << 4) | (1u << 7) | (1u << 10) | (b_rows ? 1u << 16 : 0u) |
          (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
 }
-__device__ __forceinline__ void tc_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
-                                       bool accumulate) {
+__device__ __forceinline__ void tc_mma(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc,
+                                       uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(accumulate))
+      "{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\tsetp.ne.b32 p, %5, 0;\n\t"
+      "mov.b64 x, {%1, %4};\n\tmov.b64 y, {%2, %4};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(idesc), "r"(kDescHigh), "r"(accumulate)
       : "memory");
 }
-__device__ __forceinline__ void tc_mma_tmem(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
-                                            bool accumulate) {
+__device__ __forceinline__ void tc_mma_tmem(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc,
+                                            uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(accumulate))
+      "{\n\t.reg .pred p;\n\t.reg .b64 y;\n\tsetp.ne.b32 p, %5, 0;\n\t"
+      "mov.b64 y, {%2, %4};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(idesc), "r"(kDescHigh), "r"(accumulate)
       : "memory");
+}
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t is;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(is));
+  return is != 0;
 }
 // Arrive on `bar` when the products issued so far by this thread are complete.
 __device__ __forceinline__ void tc_commit(uint64_t* bar) {
