@@ -388,7 +388,7 @@ __global__ void __launch_bounds__(32 * kRowsWarps, D == 256 ? 2 : NT == 1 ? 4 : 
         if (b < key1) raise_flag(P.s.err, kFlagSlotRange);
         page = 0;
       }
-      return static_cast<uint32_t>(row_offset(P.s, page, p) >> 3);
+      return row_off8(P.s, page, p);
     };
     auto load_k = [&](uint32_t off8) {
 #pragma unroll

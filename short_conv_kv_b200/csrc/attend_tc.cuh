@@ -29,10 +29,10 @@ struct TcShape {
 // Softmax warpgroups, producers, and a warpgroup of which one warp issues the
 // products.  Two softmax warpgroups get more registers than an even share:
 // with 16 warps of 128 launched, 2 * 184 + 2 * 72 = 4 * 128; with 20 warps
-// of 96 (MXFP8), 2 * 144 + 2 * 72 + 48 = 5 * 96.
+// of 96 (MXFP8), 2 * 136 + 2 * 64 + 80 = 5 * 96.
 template <int D, bool MX>
 __host__ __device__ constexpr int tc_threads() {
-  return 32 * (TcShape<D>::kSoftWarps + Feed<D, TcShape<D>::kKeys, MX>::kWarps + 4);
+  return 32 * (TcShape<D>::kSoftWarps + FeedShape<D, TcShape<D>::kKeys, MX>::kWarps + 4);
 }
 template <int N>
 __device__ __forceinline__ void more_registers() {
@@ -59,7 +59,7 @@ template <int D, bool MX>
 __global__ void __launch_bounds__(tc_threads<D, MX>(), 1)
     attend_tc_kernel(const AttendParams P, int rows_unit, int ring_units) {
   using T = TcShape<D>;
-  using F = Feed<D, T::kKeys, MX>;
+  using F = FeedShape<D, T::kKeys, MX>;
   constexpr int TN = T::kKeys, NS = T::kStreams, THREADS = tc_threads<D, MX>();
   constexpr int kSoft = 32 * T::kSoftWarps;
   constexpr uint32_t kQTile = 128 * D * 2, kQBlock = 128 * 128;
@@ -71,6 +71,7 @@ __global__ void __launch_bounds__(tc_threads<D, MX>(), 1)
   __shared__ float2 s_ml[2][128];
   __shared__ int64_t s_scan[THREADS / 32], s_found[2];
   __shared__ uint64_t s_full[8], s_empty[8], s_score[2], s_prob[2], s_out[2], s_query, s_drain;
+  __shared__ uint64_t s_raw_full[F::kRaw], s_raw_empty[F::kRaw];
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort[2];  // a wait ran out; a V row was cleaned
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -88,6 +89,11 @@ __global__ void __launch_bounds__(tc_threads<D, MX>(), 1)
       mbar_init(&s_prob[i], 128);
       mbar_init(&s_out[i], 1);
     }
+    if (MX)
+      for (int i = 0; i < F::kRaw; ++i) {
+        mbar_init(&s_raw_full[i], 32 * F::kFetchWarps);
+        mbar_init(&s_raw_empty[i], F::kThreads);
+      }
     mbar_init(&s_query, kSoft);
     mbar_init(&s_drain, 1);
     mbar_init_fence();
@@ -131,7 +137,7 @@ __global__ void __launch_bounds__(tc_threads<D, MX>(), 1)
 
   if (warp < T::kSoftWarps) {
     // ------------------------------------------------------------- softmax
-    if constexpr (NS == 2) more_registers<MX ? 144 : 184>();
+    if constexpr (NS == 2) more_registers<MX ? 136 : 184>();
     const int stream = warp >> 2;
     const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // this warp's lanes
     const int r = (warp & 3) * 32 + lane;                          // row of the stream's tile
@@ -394,68 +400,59 @@ __global__ void __launch_bounds__(tc_threads<D, MX>(), 1)
     if (!ok && lane == 0) raise_flag(P.s.err, kFlagTimeout);
   } else if (warp < T::kSoftWarps + F::kWarps) {
     // ------------------------------------------------------------ producers
-    if constexpr (NS == 2) fewer_registers<72>();
-    F feed;
-    {
-      FeedRing R;
-      R.units = units;
-      R.raw = raw + (tid - kSoft) * 16;
-      R.full = s_full;
-      R.empty = s_empty;
-      R.abort = s_abort;
-      R.count = ring_units;
-      feed.init(R, tid - kSoft);
-    }
-    // One unit a round; order in a segment (see the products): K0 V0 K1 V1 .. for a
-    // pair, K0 K1 V0 K2 V1 .. otherwise.
-    const uint8_t *kb = nullptr, *vb = nullptr, *ksb = nullptr, *vsb = nullptr;
-    const int32_t* table = nullptr;
-    int key0 = 0, u = 0, page = 0;
-    uint32_t off0 = ~0u, off1 = ~0u;  // of the tiles of either parity
-    tiles = 0;
-    while (true) {
-      const bool have = u < 2 * tiles || cur < end;
-      int t = 0, clean = TN;
-      bool is_v = false;
-      if (have) {
-        if (u == 2 * tiles) {  // the next segment
-          locate();
-          const int64_t head = h * P.s.stride_head;
-          kb = P.c.k + head * (MX ? 1 : 2);
-          vb = P.c.v + head * (MX ? 1 : 2);
-          ksb = MX ? P.c.ks + (head >> 5) : nullptr;
-          vsb = MX ? P.c.vs + (head >> 5) : nullptr;
-          table = P.s.table + seq * P.s.table_stride;
-          key0 = t0 * TN + feed.my_key();
-          page = __ldg(table + page_index(P.s, min(key0, total - 1)));
-          cur += tiles;
-          u = 0;
+    if constexpr (NS == 2) fewer_registers<MX ? 64 : 72>();
+    const int w = warp - T::kSoftWarps;
+    FeedRing R{units, s_full, s_empty, s_abort, ring_units};
+    if constexpr (MX) {
+      FeedRing Raw{raw, s_raw_full, s_raw_empty, s_abort, F::kRaw};
+      while (cur < end) {
+        locate();
+        const int64_t head = h * P.s.stride_head >> 5;
+        const int k_low = P.c.words ? reinterpret_cast<uintptr_t>(P.c.ks + head) & 3 : 0;
+        const int v_low = P.c.words ? reinterpret_cast<uintptr_t>(P.c.vs + head) & 3 : 0;
+#pragma unroll 1
+        for (int u = 0; u < 2 * tiles; ++u) {
+          bool is_v;
+          int t;
+          unit_of(u, tiles, pair, is_v, t);
+          const int clean = is_v ? max(0, min(TN, sv.ctx - (t0 + t) * TN)) : TN;
+          FeedMx<D, TN>::decode(R, Raw, w, lane, is_v ? v_low : k_low, clean);
         }
-        const int w = !pair && u == 2 * tiles - 1 ? u + 1 : u;
-        is_v = pair ? w & 1 : w > 0 && !(w & 1);
-        t = pair ? w >> 1 : is_v ? (w >> 1) - 1 : (w + 1) >> 1;
-        if (is_v) {
-          clean = max(0, min(TN, sv.ctx - (t0 + t) * TN));
-        } else {
-          const int p = key0 + t * TN;
-          if (static_cast<unsigned>(page) >= static_cast<unsigned>(P.s.num_pages)) {
-            if (p < total) raise_flag(P.s.err, kFlagSlotRange);
-            page = 0;
-          }
-          const uint32_t o =
-              p < total ? static_cast<uint32_t>(row_offset(P.s, page, p) >> 3) : ~0u;
-          if (t & 1) off1 = o;
-          else off0 = o;
-          page = __ldg(table + page_index(P.s, min(p + TN, total - 1)));  // of the next tile
-        }
-        ++u;
+        cur += tiles;
       }
-      if (!feed.bring(have, is_v ? vb : kb, is_v ? vsb : ksb, t & 1 ? off1 : off0, clean))
-        break;
+    } else {
+      while (cur < end) {
+        locate();
+        const int64_t head = h * P.s.stride_head;
+        const uint8_t *kb = P.c.k + head * 2, *vb = P.c.v + head * 2;
+        const int32_t* table = P.s.table + seq * P.s.table_stride;
+        const int key0 = t0 * TN + w * F::kKeysWarp + lane % F::kKeysWarp;
+        int page = __ldg(table + page_index(P.s, min(key0, total - 1)));
+        uint32_t off0 = ~0u, off1 = ~0u;  // of the tiles of either parity
+#pragma unroll 1
+        for (int u = 0; u < 2 * tiles; ++u) {
+          bool is_v;
+          int t, clean = TN;
+          unit_of(u, tiles, pair, is_v, t);
+          if (is_v) {
+            clean = max(0, min(TN, sv.ctx - (t0 + t) * TN));
+          } else {
+            const int p = key0 + t * TN;
+            const uint32_t o = paged_off8(P.s, page, p, total);
+            if (t & 1) off1 = o;
+            else off0 = o;
+            page = __ldg(table + page_index(P.s, min(p + TN, total - 1)));  // of the next tile
+          }
+          FeedBf16<D, TN>::bring(R, w, lane, is_v ? vb : kb, t & 1 ? off1 : off0, clean);
+        }
+        cur += tiles;
+      }
+      cp_commit();
+      cp_wait<0>();
     }
   } else {
     // ------------------------------------------------------------- products
-    if constexpr (NS == 2) fewer_registers<MX ? 48 : 72>();
+    if constexpr (NS == 2) fewer_registers<MX ? 80 : 72>();
     // (the whole warp goes along, so that addresses stay in uniform registers; one
     // lane issues)
     if (warp == T::kSoftWarps + F::kWarps) {
@@ -578,6 +575,51 @@ __global__ void __launch_bounds__(tc_threads<D, MX>(), 1)
     int dummy[1] = {0};
     if (!mbar_wait(&s_drain, 0, dummy, kDrainTimeoutNs)) ok = false;
     if (!ok && lane == 0) raise_flag(P.s.err, kFlagTimeout);
+    } else if constexpr (MX) {
+      // ---- raw units
+      using M = FeedMx<D, TN>;
+      const int w = warp - (T::kSoftWarps + F::kWarps + 1);
+      FeedRing Raw{raw, s_raw_full, s_raw_empty, s_abort, F::kRaw};
+      while (cur < end) {
+        locate();
+        const int64_t head = h * P.s.stride_head;
+        const int32_t* table = P.s.table + seq * P.s.table_stride;
+        const int key0 = t0 * TN + w * 8 + (lane >> 2);
+        int page[M::kMine];  // of the next tile
+        uint32_t off0[M::kMine], off1[M::kMine];  // of the tiles of either parity
+        auto pages = [&](int t) {
+#pragma unroll
+          for (int i = 0; i < M::kMine; ++i)
+            page[i] = __ldg(table + page_index(P.s, min(key0 + t * TN + i * M::kStep, total - 1)));
+        };
+        auto offsets = [&](uint32_t(&off)[M::kMine], int t) {
+#pragma unroll
+          for (int i = 0; i < M::kMine; ++i) {
+            const uint32_t o = paged_off8(P.s, page[i], key0 + t * TN + i * M::kStep, total);
+            off[i] = o == ~0u ? 0 : o;
+          }
+        };
+        pages(0);
+#pragma unroll 1
+        for (int u = 0; u < 2 * tiles; ++u) {
+          bool v;
+          int t;
+          unit_of(u, tiles, pair, v, t);
+          if (!v) {
+            if (t & 1) offsets(off1, t);
+            else offsets(off0, t);
+            pages(t + 1);
+          }
+          uint32_t off[M::kMine];
+#pragma unroll
+          for (int i = 0; i < M::kMine; ++i) off[i] = t & 1 ? off1[i] : off0[i];
+          M::fetch(Raw, w, lane, (v ? P.c.v : P.c.k) + head, (v ? P.c.vs : P.c.ks) + (head >> 5),
+                   P.c.words, off, total - (t0 + t) * TN);
+        }
+        cur += tiles;
+      }
+      cp_commit();
+      cp_wait<0>();
     }
   }
   __syncthreads();

@@ -7,7 +7,7 @@ namespace sconv {
 template <int D, bool MX>
 AttendTc tc_of(int rows) {
   using T = TcShape<D>;
-  using F = Feed<D, T::kKeys, MX>;
+  using F = FeedShape<D, T::kKeys, MX>;
   AttendTc A;
   A.fn = &attend_tc_kernel<D, MX>;
   A.threads = tc_threads<D, MX>();

@@ -73,6 +73,22 @@ __device__ __forceinline__ int64_t row_offset(const PagedSeqs& Q, int page, int 
   return page * Q.stride_page + off * Q.stride_slot;
 }
 
+// The same in units of 8 elements (below 2^32: the host checks the cache).
+__device__ __forceinline__ uint32_t row_off8(const PagedSeqs& Q, int page, int p) {
+  return static_cast<uint32_t>(page) * Q.page8 +
+         static_cast<uint32_t>(p - page_index(Q, p) * Q.page_size) * Q.slot8;
+}
+// That of a position read through `page`; ~0u at or
+// behind `total`.  A page outside the cache is flagged and read as page 0.
+__device__ __forceinline__ uint32_t paged_off8(const PagedSeqs& Q, int page, int p, int total) {
+  if (p >= total) return ~0u;
+  if (static_cast<unsigned>(page) >= static_cast<unsigned>(Q.num_pages)) {
+    raise_flag(Q.err, kFlagSlotRange);
+    page = 0;
+  }
+  return row_off8(Q, page, p);
+}
+
 // Sequence of packed token t: the largest i in [0, S-1] with cu[i] <= t.
 // One 32-way probe a round for the whole warp (all lanes, uniform t).
 __device__ __forceinline__ int warp_seq_of(const int32_t* cu, int S, int64_t t) {

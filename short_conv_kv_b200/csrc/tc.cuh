@@ -157,10 +157,13 @@ __device__ __forceinline__ uint4 lds16(uint32_t a) {
                : "memory");
   return v;
 }
-__device__ __forceinline__ uint32_t lds4(uint32_t a) {
+__device__ __forceinline__ uint32_t lds1(uint32_t a) {
   uint32_t v;
-  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
   return v;
+}
+__device__ __forceinline__ void sts1(uint32_t a, uint32_t v) {
+  asm volatile("st.shared.u8 [%0], %1;" ::"r"(a), "r"(v) : "memory");
 }
 __device__ __forceinline__ void sts16(uint32_t a, const uint4& v) {
   asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z),
@@ -217,222 +220,246 @@ __device__ __noinline__ bool e4m3x16_slow(uint4 w, uint32_t sb, bool clean, uint
   return bad;
 }
 
-// ------------------------------------------------------------ the producer
+// ------------------------------------------------------------ the producers
 //
 // A unit is a tile of KEYS cache rows of one K/V head, K's or V's, as bf16 in swizzled
 // shared memory: [D / 64][KEYS][64], each block of 64 columns in 128-byte
 // atoms.  Rows come through the block table, so they are gathered 16 bytes a
-// copy (any page size, any strides); a warp brings KEYS / kWarps whole
-// rows, whose offsets its lanes looked up.
+// copy (any page size, any strides).
 //
-// bf16: copies land in place and arrive on the unit's barrier by themselves, so
-// the ring is in flight but for the units in use.  (The thread that
-// issues the products fences the proxies behind its wait.)
-// MXFP8: a thread copies its pieces of the codes and, as an aligned word each,
-// their scale bytes into a small ring of its own, kDepth units ahead, and
-// writes them to the unit as bf16 (exact).  No thread reads another's pieces.
+// bf16: four warps bring KEYS / 4 rows each.  Copies land in place and arrive on the
+// unit's barrier by themselves, so the ring is in flight but for the units in
+// use.  (The thread that issues the products fences the proxies behind its wait.)
+// MXFP8: three warps bring the codes and scale bytes to a raw ring of kRaw
+// units, eight warps write them to the unit as bf16 (exact).  (With one kind of
+// warp for both, the addresses and copies stood between a unit's decoding and the
+// next one's: 3,200 cycles a unit instead of 1,700.)
 //
 // One call site brings all units: several copies of this code, with the
 // softmax's, fall out of the instruction cache.
 
 struct FeedRing {
   uint32_t units;  // shared-memory address of the first unit
-  uint32_t raw;    // MXFP8: this thread's pieces
   uint64_t* full;
   uint64_t* empty;
   volatile int* abort;  // [1]: a V row was cleaned
   int count;            // units in the ring
-};
 
-template <int D, int KEYS, bool MX>
-struct Feed {
-  static constexpr int kWarps = MX ? 8 : 4;
-  static constexpr int kThreads = 32 * kWarps;
-  static constexpr int kUnit = KEYS * D * 2;
-  static constexpr int kKeysWarp = KEYS / kWarps;          // rows of a warp
-  // a warp's copy: 4 (MXFP8) or 8 pieces of 16 bytes of 8 or 4 rows, a block of 64
-  // columns; neighbouring rows lie in other banks
-  static constexpr int kCols = MX ? 4 : 8;
-  static constexpr int kRowsStep = 32 / kCols;
-  static constexpr int kBlocks = D / 64;
-  static constexpr int kSteps = kKeysWarp / kRowsStep;
-  static constexpr int kPieces = kSteps * kBlocks;  // of a thread
-  static constexpr int kDepth = 3;
-  static constexpr int kRawUnit = MX ? kPieces * kThreads * 20 : 0;
-  static constexpr int kRawBytes = kDepth * kRawUnit;
-  static_assert(kKeysWarp % kRowsStep == 0 && kPieces <= 16, "");  // 2 bits a piece
-
-  FeedRing R;
-  int lane, warp, tid;
   int slot = 0, phase = 0;  // the unit to fill next
-  bool wrapped = false;
-  int pend = 0, stage = 0;  // MXFP8: units copied but not written; the raw stage of the next
-  uint32_t where[kDepth];   // MXFP8: which byte of its word a scale is, 2 bits a piece
-  int rel[kDepth];          // MXFP8: rows from here on are cleaned
-  bool ok = true;
+  bool wrapped = false, ok = true;
 
-  __device__ __forceinline__ void init(const FeedRing& ring, int t) {
-    R = ring;
-    tid = t;
-    lane = t & 31;
-    warp = t >> 5;
-#pragma unroll
-    for (int i = 0; i < kDepth; ++i) {
-      where[i] = 0;
-      rel[i] = KEYS;
-    }
-  }
-  __device__ __forceinline__ int my_key() const { return warp * kKeysWarp + lane % kKeysWarp; }
   __device__ __forceinline__ void wait_empty() {
-    if (wrapped && ok && !mbar_wait(R.empty + slot, phase, R.abort, kTcTimeoutNs)) ok = false;
+    if (wrapped && ok && !mbar_wait(empty + slot, phase, abort, kTcTimeoutNs)) ok = false;
   }
   __device__ __forceinline__ void advance() {
-    if (++slot == R.count) {
+    if (++slot == count) {
       slot = 0;
       if (wrapped) phase ^= 1;
       wrapped = true;
     }
   }
-  __device__ __forceinline__ int row_of(int i) const {  // of piece i
-    return warp * kKeysWarp + i / kBlocks * kRowsStep + lane / kCols;
-  }
-  // where 8 columns go: block i % kBlocks of piece i, chunk of 16 bytes in it
-  __device__ __forceinline__ uint32_t place(int i, int chunk) const {
-    const int key = row_of(i);
-    return R.units + slot * kUnit + i % kBlocks * (KEYS * 128) + key * 128 +
-           ((chunk ^ (key & 7)) << 4);
-  }
+};
 
-  __device__ __forceinline__ void bring_bf16(const uint8_t* base, uint32_t off8, int clean) {
-    wait_empty();
-    const int chunk = lane % kCols;
+// Threads that make a unit, those that fetch its raw bytes, and what they hold
+// of shared memory besides.
+template <int D, int KEYS, bool MX>
+struct FeedShape {
+  static constexpr int kWarps = MX ? 8 : 4;
+  static constexpr int kThreads = 32 * kWarps;
+  static constexpr int kUnit = KEYS * D * 2;
+  static constexpr int kKeysWarp = KEYS / kWarps;  // rows of a warp
+  static constexpr int kBlocks = D / 64;
+  // a warp's step: 4 (MXFP8) or 8 pieces of 16 bytes of 8 or 4 rows, one block
+  static constexpr int kCols = MX ? 4 : 8;
+  static constexpr int kRowsStep = 32 / kCols;
+  static constexpr int kSteps = kKeysWarp / kRowsStep;
+  static constexpr int kRaw = 3;          // units in the raw ring
+  static constexpr int kFetchWarps = 3;
+  static constexpr int kScaleRow = 16;    // bytes of a raw row's scales
+  static constexpr int kRawUnit = MX ? KEYS * (D + kScaleRow) : 0;
+  static constexpr int kRawBytes = kRaw * kRawUnit;
+  static_assert(kKeysWarp % kRowsStep == 0, "");
+};
+
+template <int D, int KEYS>
+struct FeedBf16 : FeedShape<D, KEYS, false> {
+  using S = FeedShape<D, KEYS, false>;
+  // One unit: off8 is the offset, in units of 8 elements, of the row of key
+  // warp * kKeysWarp + lane % kKeysWarp, ~0u for a row of zeros; rows at or behind
+  // `clean` lose NaN and infinities.
+  static __device__ __forceinline__ void bring(FeedRing& R, int warp, int lane,
+                                               const uint8_t* base, uint32_t off8, int clean) {
+    R.wait_empty();
+    const int chunk = lane % S::kCols;
     const uint8_t* col = base + chunk * 16;
+    const int row0 = warp * S::kKeysWarp + lane / S::kCols;
+    auto place = [&](int j, int b) {
+      const int key = row0 + j * S::kRowsStep;
+      return R.units + R.slot * S::kUnit + b * (KEYS * 128) + key * 128 +
+             ((chunk ^ (key & 7)) << 4);
+    };
 #pragma unroll
-    for (int j = 0; j < kSteps; ++j) {
-      const uint32_t o = __shfl_sync(kFullMask, off8, j * kRowsStep + lane / kCols);
+    for (int j = 0; j < S::kSteps; ++j) {
+      const uint32_t o = __shfl_sync(kFullMask, off8, j * S::kRowsStep + lane / S::kCols);
       const uint8_t* from = col + (o == ~0u ? 0 : static_cast<uint64_t>(o) * 16);
 #pragma unroll
-      for (int b = 0; b < kBlocks; ++b)
-        if (ok) cp16(place(j * kBlocks + b, chunk), from + b * 128, o != ~0u);
+      for (int b = 0; b < S::kBlocks; ++b)
+        if (R.ok) cp16(place(j, b), from + b * 128, o != ~0u);
     }
     if (clean >= KEYS) {
-      cp_arrive(R.full + slot);
+      cp_arrive(R.full + R.slot);
     } else {
       cp_commit();
       cp_wait<0>();
 #pragma unroll 1
-      for (int i = 0; i < kPieces; ++i)
-        if (row_of(i) >= clean) {
-          const uint32_t a = place(i, chunk);
+      for (int j = 0; j < S::kSteps; ++j) {
+        if (row0 + j * S::kRowsStep < clean) continue;
+#pragma unroll 1
+        for (int b = 0; b < S::kBlocks; ++b) {
           bool bad = false;
-          const uint4 v = clean16<false>(lds16(a), bad);
+          const uint4 v = clean16<false>(lds16(place(j, b)), bad);
           if (bad) {
-            sts16(a, v);
+            sts16(place(j, b), v);
             R.abort[1] = 1;
           }
         }
+      }
       async_proxy_fence();
-      mbar_arrive(R.full + slot);
+      mbar_arrive(R.full + R.slot);
     }
-    advance();
+    R.advance();
+  }
+};
+
+// Raw unit: codes [D / 64][KEYS][64], then the scales, kScaleRow bytes a row from
+// its first aligned word on.  The scale bytes begin `low` bytes into
+// that word, the same for all rows (`words`), or at 0, copied one by one.
+template <int D, int KEYS>
+struct FeedMx : FeedShape<D, KEYS, true> {
+  using S = FeedShape<D, KEYS, true>;
+  static constexpr int kGroups = KEYS / 8;  // of eight rows
+  static constexpr int kMine = (kGroups + S::kFetchWarps - 1) / S::kFetchWarps;
+  static constexpr int kScales = KEYS * D;  // where a raw unit's scales begin
+
+  // Fetching warp w's part of a raw unit: the rows of keys kStep * i + w * 8 + lane / 4
+  // at offsets off[i] (units of 8 elements); zeros for keys from `left` on.
+  static constexpr int kStep = 8 * S::kFetchWarps;
+  static __device__ __forceinline__ void fetch(FeedRing& R, int w, int lane, const uint8_t* base,
+                                               const uint8_t* scales, bool words,
+                                               const uint32_t (&off)[kMine], int left) {
+    R.wait_empty();
+    const int c = lane & 3, key = w * 8 + (lane >> 2);
+    const uint32_t unit = R.units + R.slot * S::kRawUnit;
+    const uint32_t to = unit + w * 512 + lane * 16;
+    const uint32_t st = unit + kScales + key * S::kScaleRow + c * 4;
+    const uint8_t* from = base + c * 16;
+    if (R.ok && words) {
+      const int low = static_cast<int>(reinterpret_cast<uintptr_t>(scales) & 3u);
+      const bool mine = c * 4 < low + D / 32;
+      const uint8_t* sp = scales - low + c * 4;
+#pragma unroll
+      for (int i = 0; i < kMine; ++i) {
+        if (i == kMine - 1 && kGroups % S::kFetchWarps && w + S::kFetchWarps * i >= kGroups) break;
+        const bool there = key + i * kStep < left;
+        const uint8_t* f = from + static_cast<uint64_t>(off[i]) * 8;
+#pragma unroll
+        for (int b = 0; b < S::kBlocks; ++b)
+          cp16(to + b * (KEYS * 64) + i * (S::kFetchWarps * 512), f + b * 64, there);
+        if (mine) cp4(st + i * (kStep * S::kScaleRow), sp + (off[i] >> 2), there);
+      }
+      cp_arrive(R.full + R.slot);
+    } else {
+      if (R.ok) {
+#pragma unroll 1
+        for (int i = 0; i < kMine && w + S::kFetchWarps * i < kGroups; ++i) {
+          uint32_t o = 0;
+#pragma unroll
+          for (int k = 0; k < kMine; ++k) o = k == i ? off[k] : o;
+          const bool there = key + i * kStep < left;
+          const uint8_t* f = from + static_cast<uint64_t>(o) * 8;
+#pragma unroll 1
+          for (int b = 0; b < S::kBlocks; ++b)
+            cp16(to + b * (KEYS * 64) + i * (S::kFetchWarps * 512), f + b * 64, there);
+          for (int b = c; b < D / 32; b += 4)
+            sts1(st - c * 4 + i * (kStep * S::kScaleRow) + b,
+                 there ? __ldg(scales + (o >> 2) + b) : 0u);
+        }
+      }
+      cp_commit();
+      cp_wait<0>();
+      mbar_arrive(R.full + R.slot);
+    }
+    R.advance();
   }
 
-  __device__ __forceinline__ uint32_t raw_at(int st, int i) const {
-    return R.raw + st * kRawUnit + i * (kThreads * 16);
-  }
-  __device__ __forceinline__ uint32_t scale_at(int st, int i) const {
-    return R.raw - tid * 16 + st * kRawUnit + kPieces * kThreads * 16 + i * (kThreads * 4) + tid * 4;
-  }
-  __device__ __forceinline__ void write_unit(int st, uint32_t bytes, int clean) {
-    wait_empty();
-    if (ok) {
-      const int chunk = (lane % kCols) * 2;
+  // The next raw unit to the next unit.
+  static __device__ __forceinline__ void decode(FeedRing& R, FeedRing& Raw, int warp, int lane,
+                                                int low, int clean) {
+    if (Raw.ok && !mbar_wait(Raw.full + Raw.slot, Raw.phase, Raw.abort, kTcTimeoutNs)) Raw.ok = false;
+    R.wait_empty();
+    if (R.ok && Raw.ok) {
+      const int chunk = (lane & 3) * 2, row0 = warp * S::kKeysWarp + (lane >> 2);
       uint32_t sixteen = 16u, one = 1u;
       asm volatile("" : "+r"(sixteen), "+r"(one));
-#pragma unroll kBlocks
+      const uint32_t raw = Raw.units + Raw.slot * S::kRawUnit;
+      auto place = [&](int j, int b, int c) {
+        const int key = row0 + j * 8;
+        return R.units + R.slot * S::kUnit + b * (KEYS * 128) + key * 128 + ((c ^ (key & 7)) << 4);
+      };
+      constexpr int kPieces = S::kSteps * S::kBlocks;
+      uint4 w[kPieces];
+      uint32_t sb[kPieces];
+#pragma unroll
       for (int i = 0; i < kPieces; ++i) {
-        const uint4 w = lds16(raw_at(st, i));
-        const uint32_t sb = (lds4(scale_at(st, i)) >> (8 * ((bytes >> (2 * i)) & 3u))) & 255u;
-        const uint32_t both = (sb + 120u) * 0x00800080u;
-        uint4 a, b;
-        uint2 nan = make_uint2(0u, 0u);
-        e4m3x4_bf16_fast(w.x, both, sixteen, one, a.x, a.y, nan);
-        e4m3x4_bf16_fast(w.y, both, sixteen, one, a.z, a.w, nan);
-        e4m3x4_bf16_fast(w.z, both, sixteen, one, b.x, b.y, nan);
-        e4m3x4_bf16_fast(w.w, both, sixteen, one, b.z, b.w, nan);
-        if ((nan.x & 0x00800080u) || (nan.y & 0x08000800u) || sb > 134u) {
+        const int j = i / S::kBlocks, b = i % S::kBlocks;
+        w[i] = lds16(raw + b * (KEYS * 64) + (row0 + j * 8) * 64 + (lane & 3) * 16);
+        sb[i] = lds1(raw + kScales + (row0 + j * 8) * S::kScaleRow + low + b * 2 + ((lane & 3) >> 1));
+      }
+      uint2 nan = make_uint2(0u, 0u);
+      uint32_t top = 0;
+#pragma unroll
+      for (int i = 0; i < kPieces; ++i) {
+        const int j = i / S::kBlocks, b = i % S::kBlocks;
+        const uint32_t both = (sb[i] + 120u) * 0x00800080u;
+        uint4 x, y;
+        e4m3x4_bf16_fast(w[i].x, both, sixteen, one, x.x, x.y, nan);
+        e4m3x4_bf16_fast(w[i].y, both, sixteen, one, x.z, x.w, nan);
+        e4m3x4_bf16_fast(w[i].z, both, sixteen, one, y.x, y.y, nan);
+        e4m3x4_bf16_fast(w[i].w, both, sixteen, one, y.z, y.w, nan);
+        top = max(top, sb[i]);
+        sts16(place(j, b, chunk), x);
+        sts16(place(j, b, chunk + 1), y);
+      }
+      if ((nan.x & 0x00800080u) || (nan.y & 0x08000800u) || top > 134u) {  // rare: once more
+#pragma unroll 1
+        for (int i = 0; i < kPieces; ++i) {
+          const int j = i / S::kBlocks, b = i % S::kBlocks;
+          const uint4 v = lds16(raw + b * (KEYS * 64) + (row0 + j * 8) * 64 + (lane & 3) * 16);
+          const uint32_t s = lds1(raw + kScales + (row0 + j * 8) * S::kScaleRow + low + b * 2 + ((lane & 3) >> 1));
           uint4 x[2];
-          if (e4m3x16_slow(w, sb, row_of(i) >= clean, x)) R.abort[1] = 1;
-          a = x[0];
-          b = x[1];
+          if (e4m3x16_slow(v, s, row0 + j * 8 >= clean, x)) R.abort[1] = 1;
+          sts16(place(j, b, chunk), x[0]);
+          sts16(place(j, b, chunk + 1), x[1]);
         }
-        sts16(place(i, chunk), a);
-        sts16(place(i, chunk + 1), b);
       }
     }
     async_proxy_fence();
-    mbar_arrive(R.full + slot);
-    advance();
-  }
-  __device__ __forceinline__ void bring_mx(bool have, const uint8_t* base, const uint8_t* scales,
-                                           uint32_t off8, int clean) {
-    if (have) {
-      const int chunk = lane % kCols;
-      uint32_t bytes = 0;
-#pragma unroll
-      for (int j = 0; j < kSteps; ++j) {
-        const uint32_t o = __shfl_sync(kFullMask, off8, j * kRowsStep + lane / kCols);
-        const uint64_t o8 = o == ~0u ? 0 : o;
-        const uint8_t* from = base + o8 * 8 + chunk * 16;
-        const uint8_t* sp = scales + (o8 >> 2) + (chunk >> 1);
-#pragma unroll
-        for (int b = 0; b < kBlocks; ++b) {
-          const int i = j * kBlocks + b;
-          const uint32_t low =
-              static_cast<uint32_t>(reinterpret_cast<uintptr_t>(sp + 2 * b)) & 3u;
-          if (ok) {
-            cp16(raw_at(stage, i), from + b * 64, o != ~0u);
-            cp4(scale_at(stage, i), sp + 2 * b - low, o != ~0u);
-          }
-          bytes |= low << (2 * i);
-        }
-      }
-      where[0] = bytes;
-      rel[0] = clean;
-      ++pend;
-    }
-    // an empty group too, so that the oldest unit is always kDepth - 1 groups back
-    cp_commit();
-    stage = stage + 1 == kDepth ? 0 : stage + 1;
-    if (pend == kDepth || (!have && pend)) {
-      cp_wait<kDepth - 1>();
-      write_unit(stage, where[kDepth - 1], rel[kDepth - 1]);
-      --pend;
-    }
-#pragma unroll
-    for (int i = kDepth - 1; i > 0; --i) {
-      where[i] = where[i - 1];
-      rel[i] = rel[i - 1];
-    }
-  }
-
-  // One unit (with `have`): off8 is the offset, in units of 8 elements, of the row
-  // of my_key(), ~0u for a row of zeros; rows at or behind `clean` lose NaN and
-  // infinities.  Without: go on with what is under way.  False when nothing is.
-  __device__ __forceinline__ bool bring(bool have, const uint8_t* base, const uint8_t* scales,
-                                        uint32_t off8, int clean) {
-    if constexpr (MX) {
-      bring_mx(have, base, scales, off8, clean);
-      return have || pend > 0;
-    } else {
-      if (have) bring_bf16(base, off8, clean);
-      else {
-        cp_commit();
-        cp_wait<0>();
-      }
-      return have;
+    mbar_arrive(R.full + R.slot);
+    R.advance();
+    mbar_arrive(Raw.empty + Raw.slot);
+    if (++Raw.slot == Raw.count) {
+      Raw.slot = 0;
+      Raw.phase ^= 1;
     }
   }
 };
+
+// Unit u of a segment of `tiles` key tiles, in the order in which the products need
+// them: K0 V0 K1 V1 .. for a pair of streams, K0 K1 V0 K2 V1 .. otherwise.
+__device__ __forceinline__ void unit_of(int u, int tiles, bool pair, bool& is_v, int& t) {
+  const int w = !pair && u == 2 * tiles - 1 ? u + 1 : u;
+  is_v = pair ? w & 1 : w > 0 && !(w & 1);
+  t = pair ? w >> 1 : is_v ? (w >> 1) - 1 : (w + 1) >> 1;
+}
 
 }  // namespace sconv

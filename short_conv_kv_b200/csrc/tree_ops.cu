@@ -73,6 +73,8 @@ int check_paged(const sconv_kv_paged_t* seqs, const sconv_kv_cache_layout_t* lay
   Q->stride_page = layout->stride_page;
   Q->stride_slot = layout->stride_slot;
   Q->stride_head = layout->stride_head;
+  Q->page8 = static_cast<uint32_t>(layout->stride_page / 8);
+  Q->slot8 = static_cast<uint32_t>(layout->stride_slot / 8);
   Q->err = err;
   return SCONV_KV_OK;
 }
@@ -99,8 +101,9 @@ CacheParts parts_of(const void* k, const void* v, const void* ks, const void* vs
   const bool packed = ks && aligned(ks, static_cast<size_t>(row)) &&
                       layout->stride_head / 32 % row == 0 && layout->stride_slot / 32 % row == 0 &&
                       layout->stride_page / 32 % row == 0;
+  const bool words = layout->stride_slot / 32 % 4 == 0 && layout->stride_page / 32 % 4 == 0;
   auto raw = [](const void* p) { return const_cast<uint8_t*>(static_cast<const uint8_t*>(p)); };
-  return {raw(k), raw(v), raw(ks), raw(vs), packed ? 1 : 0};
+  return {raw(k), raw(v), raw(ks), raw(vs), packed ? 1 : 0, words ? 1 : 0};
 }
 
 int check_heads(int HQ, int H, int64_t tok, int64_t head, int D) {

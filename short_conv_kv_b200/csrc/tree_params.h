@@ -27,6 +27,8 @@ struct PagedSeqs {
   int64_t stride_page;  // elements
   int64_t stride_slot;
   int64_t stride_head;
+  uint32_t page8;  // stride_page and stride_slot in units of 8 elements
+  uint32_t slot8;
   int* err;
 };
 
@@ -37,6 +39,7 @@ struct CacheParts {
   uint8_t* ks;
   uint8_t* vs;
   int ks_packed;  // a row's D/32 K scales can be loaded at once (aligned)
+  int words;      // a head's scales begin at the same byte of a 4-byte word in every row
 };
 
 struct TreeStepParams {

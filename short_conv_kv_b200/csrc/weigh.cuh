@@ -104,7 +104,7 @@ __global__ void __launch_bounds__(32 * kWeighWarps, D == 256 ? 2 : 3)
           if (b < key1) raise_flag(P.s.err, kFlagSlotRange);
           page = 0;
         }
-        return static_cast<uint32_t>(row_offset(P.s, page, p) >> 3);
+        return row_off8(P.s, page, p);
       };
       auto load_k = [&](uint32_t off8) {
 #pragma unroll
