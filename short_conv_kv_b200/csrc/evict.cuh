@@ -5,14 +5,27 @@
 // ties to the lowest position; the kept rows move to positions 0 .. keep-1 in
 // their order.
 //
-// Selection (evict_select_kernel): the weight as an order-preserving 32-bit
-// key, the k-th largest key found 8 bits at a time from histograms in shared
-// memory, then one pass in position order that writes the kept positions and
-// their weights.  Movement (evict_move_kernel): see there.
+// Both kernels give a (sequence, head) to a cluster of CTAs, one when there are
+// enough of them to fill the GPU, up to eight for a single long sequence.
+//
+// Selection: the weight as an order-preserving 32-bit key, the k-th largest key
+// found 8 bits at a time from histograms in shared memory, which the cluster's
+// CTAs, a slice of the positions each, read from one another; then the positions
+// in order, a warp a stretch: counted, scanned over warps and CTAs, written.  The
+// keys stay in shared memory when a slice fits.  It reads 4 bytes a position and is
+// bound by the latency of its seven steps.
+//
+// Movement: in place, so it goes up in rounds.  All of a round's rows are
+// loaded by the cluster before any of them is stored; a later round's sources lie
+// at or behind its own targets (kept[j] >= j), which no earlier round writes.
 #pragma once
+#include <cooperative_groups.h>
+
 #include "paged.cuh"
 
 namespace sconv {
+
+namespace cg = cooperative_groups;
 
 // Key whose unsigned order is the weight's: -0 equals +0, NaN above +inf.
 __device__ __forceinline__ uint32_t weight_key(float w) {
@@ -21,50 +34,83 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-
-// One block a (sequence, head).
-__global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const EvictParams A) {
+// grid (CTAs of a cluster * H, S); dynamic shared memory: room for `room` keys.
+__global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const EvictParams A, int room) {
+  constexpr int kWarps = kSelectThreads / 32;
   grid_dependency_wait();
   allow_dependent_launch();
-  __shared__ uint32_t hist[256];
+  const cg::cluster_group cluster = cg::this_cluster();
+  const int ctas = static_cast<int>(cluster.num_blocks());
+  const int rank = static_cast<int>(cluster.block_rank());
+  extern __shared__ uint32_t s_keys[];
+  __shared__ uint32_t s_hist[2][256], s_all[256];
   __shared__ uint32_t s_prefix;
   __shared__ int s_need;
-  __shared__ int s_warp[2][kSelectThreads / 32];
-  const int h = blockIdx.x, i = blockIdx.y;
+  __shared__ int2 s_count[kWarps];  // more, equal
+  __shared__ int2 s_slice;
+  const int h = blockIdx.x / ctas, i = blockIdx.y;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const bool lead = h == 0 && tid == 0;
+  const bool lead = h == 0 && rank == 0 && tid == 0;
   const SeqView s = seq_view(A.q, i, lead);
-  if (!s.ok) return;
+  if (!s.ok) return;  // the whole cluster
   const int len = s.ctx;
   if (lead) A.new_lens[i] = min(len, A.keep);
   const float* w = A.weights + i * A.w_seq + h * A.w_head;
   float* wo = A.weights_out ? A.weights_out + i * A.o_seq + h * A.o_head : nullptr;
   int32_t* kept = A.kept + (static_cast<int64_t>(i) * A.H + h) * A.keep;
   if (len <= A.keep) {
-    for (int p = tid; p < A.keep; p += kSelectThreads) {
+    for (int p = rank * kSelectThreads + tid; p < A.keep; p += ctas * kSelectThreads) {
       kept[p] = p < len ? p : -1;
       if (wo && p < len) wo[p] = w[p];
     }
     return;
   }
+  // this CTA's slice of the positions, and a warp's stretch of it (multiples of 32)
+  const int stretch = ((len / ctas + 1 + kWarps - 1) / kWarps + 31) & ~31;
+  const int64_t slice = static_cast<int64_t>(stretch) * kWarps;
+  auto at_most = [](int64_t x, int y) { return x < y ? static_cast<int>(x) : y; };
+  const int a = at_most(static_cast<int64_t>(rank) * slice, len);
+  const int e = at_most(static_cast<int64_t>(a) + slice, len);
   const int lo = A.sinks, hi = len - A.recent;  // candidates
-  int need = A.keep - A.sinks - A.recent;       // 0 <= need < hi - lo
+  const bool held = e - a <= room;
+  if (held) {
+#pragma unroll 4
+    for (int p = a + tid; p < e; p += kSelectThreads) s_keys[p - a] = weight_key(w[p]);
+  }
+  for (int b = tid; b < 512; b += kSelectThreads) (&s_hist[0][0])[b] = 0;
+  __syncthreads();
+  auto key_at = [&](int p) { return held ? s_keys[p - a] : weight_key(w[p]); };
+  const bool any = A.keep - A.sinks - A.recent > 0;
+  int need = A.keep - A.sinks - A.recent;  // 0 <= need < hi - lo
   uint32_t prefix = 0;
-  if (need > 0) {
-    for (int shift = 24; shift >= 0; shift -= 8) {
-      for (int b = tid; b < 256; b += kSelectThreads) hist[b] = 0;
-      __syncthreads();
-      const uint32_t above = shift == 24 ? 0u : 0xffffffffu << (shift + 8);
-      for (int p = lo + tid; p < hi; p += kSelectThreads) {
-        const uint32_t key = weight_key(w[p]);
-        if ((key & above) == prefix) atomicAdd(&hist[(key >> shift) & 255u], 1u);
+  if (any) {
+    const int c0 = max(a, lo), c1 = min(e, hi);
+    for (int step = 0; step < 4; ++step) {
+      const int shift = 24 - 8 * step;
+      uint32_t* hist = s_hist[step & 1];
+      const uint32_t above = step == 0 ? 0u : 0xffffffffu << (shift + 8);
+      for (int p = c0 + warp * 32; p < c1; p += kSelectThreads) {
+        const bool in = p + lane < c1;
+        const uint32_t key = in ? key_at(p + lane) : 0u;
+        const bool mine = in && (key & above) == prefix;
+        const uint32_t bin = mine ? (key >> shift) & 255u : 256u;
+        // equal bins (weights are often equal) are added once a warp
+        const unsigned same = __match_any_sync(kFullMask, bin);
+        if (mine && lane == __ffs(same) - 1) atomicAdd(&hist[bin], __popc(same));
+      }
+      cluster.sync();
+      if (tid < 256) {
+        uint32_t sum = 0;
+        for (int c = 0; c < ctas; ++c) sum += cluster.map_shared_rank(hist, c)[tid];
+        s_all[tid] = sum;
+        s_hist[(step + 1) & 1][tid] = 0;  // last read before the sync above
       }
       __syncthreads();
       if (warp == 0) {  // the bin that the need-th largest falls in
         uint32_t own[8], sum = 0;
 #pragma unroll
         for (int b = 0; b < 8; ++b) {  // lane l holds bins 255-8l .. 248-8l
-          own[b] = hist[255 - 8 * lane - b];
+          own[b] = s_all[255 - 8 * lane - b];
           sum += own[b];
         }
         uint32_t before = sum;
@@ -77,7 +123,12 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const Evic
         const uint32_t want = static_cast<uint32_t>(need);
         if (before < want && want <= before + sum) {
           int b = 0;
-          while (before + own[b] < want) before += own[b++];
+#pragma unroll
+          for (int k = 0; k < 7; ++k)
+            if (b == k && before + own[k] < want) {
+              before += own[k];
+              ++b;
+            }
           s_prefix = prefix | (static_cast<uint32_t>(255 - 8 * lane - b) << shift);
           s_need = need - static_cast<int>(before);
         }
@@ -87,117 +138,148 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const Evic
       need = s_need;
     }
   }
-  // prefix: the key of the last kept; `need` of those equal to it are kept
-  const bool any = A.keep - A.sinks - A.recent > 0;
-  int taken = 0, equal = 0;  // before this chunk
-  for (int base = 0; base < len; base += kSelectThreads) {
-    const int p = base + tid;
-    float x = 0.f;
-    bool more = false, same = false;
-    if (p < len) {
-      x = w[p];
-      if (p < lo || p >= hi) {
-        more = true;
-      } else if (any) {
-        const uint32_t key = weight_key(x);
-        more = key > prefix;
-        same = key == prefix;
+  // prefix: the key of the last kept; the first `need` of those equal to it are kept
+  const int p0 = at_most(static_cast<int64_t>(a) + warp * stretch, e);
+  const int p1 = at_most(static_cast<int64_t>(p0) + stretch, e);
+  auto classify = [&](int p, bool& more, bool& same) {
+    more = same = false;
+    if (p >= p1) return;
+    if (p < lo || p >= hi) {
+      more = true;
+    } else if (any) {
+      const uint32_t key = key_at(p);
+      more = key > prefix;
+      same = key == prefix;
+    }
+  };
+  int2 count = make_int2(0, 0);
+  for (int p = p0; p < p1; p += 32) {
+    bool more, same;
+    classify(p + lane, more, same);
+    count.x += __popc(__ballot_sync(kFullMask, more));
+    count.y += __popc(__ballot_sync(kFullMask, same));
+  }
+  if (lane == 0) s_count[warp] = count;
+  __syncthreads();
+  int2 before = make_int2(0, 0);
+  if (warp == 0) {
+    int2 c = s_count[lane];
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int x = __shfl_up_sync(kFullMask, c.x, d), y = __shfl_up_sync(kFullMask, c.y, d);
+      if (lane >= d) {
+        c.x += x;
+        c.y += y;
       }
     }
-    const unsigned bs = __ballot_sync(kFullMask, same);
-    if (lane == 0) s_warp[0][warp] = __popc(bs);
-    __syncthreads();
-    int eq = equal, eq_all = equal;
-    for (int k = 0; k < kSelectThreads / 32; ++k) {
-      const int v = s_warp[0][k];
-      if (k < warp) eq += v;
-      eq_all += v;
-    }
-    eq += __popc(bs & ((1u << lane) - 1u));
-    const bool keep = more || (same && eq < need);
-    const unsigned bk = __ballot_sync(kFullMask, keep);
-    if (lane == 0) s_warp[1][warp] = __popc(bk);
-    __syncthreads();
-    int at = taken, at_all = taken;
-    for (int k = 0; k < kSelectThreads / 32; ++k) {
-      const int v = s_warp[1][k];
-      if (k < warp) at += v;
-      at_all += v;
-    }
-    at += __popc(bk & ((1u << lane) - 1u));
-    if (keep) {
-      kept[at] = p;
-      if (wo) wo[at] = x;
-    }
-    taken = at_all;
-    equal = eq_all;
-    __syncthreads();
+    if (lane == 31) s_slice = c;
+    const int2 own = s_count[lane];
+    s_count[lane] = make_int2(c.x - own.x, c.y - own.y);
   }
+  cluster.sync();
+  for (int c = 0; c < rank; ++c) {
+    const int2 v = *cluster.map_shared_rank(&s_slice, c);
+    before.x += v.x;
+    before.y += v.y;
+  }
+  int more_at = before.x + s_count[warp].x, same_at = before.y + s_count[warp].y;
+  for (int p = p0; p < p1; p += 32) {
+    bool more, same;
+    classify(p + lane, more, same);
+    const unsigned bm = __ballot_sync(kFullMask, more), bs = __ballot_sync(kFullMask, same);
+    const unsigned lower = (1u << lane) - 1u;
+    const int rank_same = same_at + __popc(bs & lower);
+    const int at = more_at + __popc(bm & lower) + min(rank_same, need);
+    if (more || (same && rank_same < need)) {
+      kept[at] = p + lane;
+      if (wo) wo[at] = w[p + lane];
+    }
+    more_at += __popc(bm);
+    same_at += __popc(bs);
+  }
+  cluster.sync();  // nobody leaves while its counts may be read
 }
 
-// Rows kept[j] -> j of one cache part, in place.  A block owns one slice of
-// the row's bytes of one (sequence, head, part) and walks j upwards in
-// chunks: a chunk is loaded whole before any of it is stored, and every
-// source of a later chunk lies at or behind that chunk's first target
-// (kept[j] >= j), so no row is overwritten before it is read.
-constexpr int kMoveRows = 8;  // rows in flight a thread
+// A row's scale bytes, one access where they are aligned.
+template <typename SC>
+__device__ __forceinline__ SC load_scales(const uint8_t* p, bool packed) {
+  if (packed) return *reinterpret_cast<const SC*>(p);
+  SC v = 0;
+#pragma unroll
+  for (int b = 0; b < static_cast<int>(sizeof(SC)); ++b) v |= static_cast<SC>(p[b]) << (8 * b);
+  return v;
+}
+template <typename SC>
+__device__ __forceinline__ void store_scales(uint8_t* p, SC v, bool packed) {
+  if (packed) {
+    *reinterpret_cast<SC*>(p) = v;
+    return;
+  }
+#pragma unroll
+  for (int b = 0; b < static_cast<int>(sizeof(SC)); ++b) p[b] = static_cast<uint8_t>(v >> (8 * b));
+}
 
-template <typename V>
-__device__ __forceinline__ void move_rows(const EvictParams& A, uint8_t* base, int i, int h,
-                                          const int32_t* kept, int keep, int vecs, int col_bytes,
-                                          int num, int den) {
-  // byte address of element offset e: e * num / den
-  const int per = kMoveThreads / vecs;  // rows side by side
-  const int r = threadIdx.x / vecs, x = threadIdx.x - r * vecs;
+// grid (CTAs of a cluster * 2 * H, S): K's or V's rows of one head, with their
+// scales (MXFP8).  A thread has one 16-byte piece of kMoveRows rows a round.
+// DB: bytes of a row; SC: its scales as one number (bf16: unused).
+constexpr int kMoveRows = 8;
+
+template <int DB, bool MX, typename SC>
+__global__ void __launch_bounds__(kMoveThreads, 2) evict_move_kernel(const EvictParams A) {
+  grid_dependency_wait();
+  allow_dependent_launch();
+  const cg::cluster_group cluster = cg::this_cluster();
+  const int ctas = static_cast<int>(cluster.num_blocks());
+  const int rank = static_cast<int>(cluster.block_rank());
+  const int unit = blockIdx.x / ctas, h = unit >> 1, i = blockIdx.y;
+  const SeqView s = seq_view(A.q, i, false);
+  if (!s.ok || s.ctx <= A.keep) return;  // the whole cluster
+  constexpr int kVecs = DB / 16, kSide = kMoveThreads / kVecs, kChunk = kSide * kMoveRows;
+  const int r = threadIdx.x / kVecs, x = threadIdx.x % kVecs;
+  const int32_t* kept = A.kept + (static_cast<int64_t>(i) * A.H + h) * A.keep;
+  const int32_t* table = A.q.table + i * A.q.table_stride;
   const int64_t head = h * A.q.stride_head;
-  for (int j0 = 0; j0 < keep; j0 += per * kMoveRows) {
-    V buf[kMoveRows];
-    bool mv[kMoveRows];
+  uint8_t* base = ((unit & 1) ? A.c.v : A.c.k) + head * (MX ? 1 : 2) + x * 16;
+  uint8_t* scales = MX ? ((unit & 1) ? A.c.vs : A.c.ks) + (head >> 5) : nullptr;
+  const bool packed = A.c.scales_packed;
+  auto offset = [&](int p) {  // ~0u for a page outside the cache
+    const int page = __ldg(table + page_index(A.q, p));
+    if (static_cast<unsigned>(page) >= static_cast<unsigned>(A.q.num_pages)) {
+      raise_flag(A.q.err, kFlagSlotRange);
+      return ~0u;
+    }
+    return row_off8(A.q, page, p);
+  };
+  for (int j0 = rank * kChunk; j0 - rank * kChunk < A.keep; j0 += ctas * kChunk) {
+    uint4 buf[kMoveRows];
+    SC sc[kMoveRows];
+    uint32_t to[kMoveRows];
+    int from[kMoveRows];
 #pragma unroll
     for (int u = 0; u < kMoveRows; ++u) {
-      const int j = j0 + u * per + r;
-      mv[u] = false;
-      if (r < per && j < keep) {
-        const int p = kept[j];
-        if (p > j) {
-          const int page = page_of(A.q, i, p, true);
-          if (page >= 0) {
-            mv[u] = true;
-            buf[u] = *reinterpret_cast<const V*>(
-                base + (row_offset(A.q, page, p) + head) * num / den + col_bytes + x * sizeof(V));
-          }
+      const int j = j0 + u * kSide + r;
+      from[u] = j < A.keep ? __ldg(kept + j) : -1;
+    }
+#pragma unroll
+    for (int u = 0; u < kMoveRows; ++u) {
+      const int j = j0 + u * kSide + r;
+      to[u] = ~0u;
+      if (from[u] > j) {
+        const uint32_t f = offset(from[u]);
+        if (f != ~0u) {
+          to[u] = offset(j);
+          buf[u] = *reinterpret_cast<const uint4*>(base + static_cast<uint64_t>(f) * (MX ? 8 : 16));
+          if (MX && x == 0) sc[u] = load_scales<SC>(scales + (f >> 2), packed);
         }
       }
     }
-    __syncthreads();
+    cluster.sync();
 #pragma unroll
-    for (int u = 0; u < kMoveRows; ++u) {
-      const int j = j0 + u * per + r;
-      if (mv[u]) {
-        const int page = page_of(A.q, i, j, true);
-        if (page >= 0)
-          *reinterpret_cast<V*>(base + (row_offset(A.q, page, j) + head) * num / den + col_bytes +
-                                x * sizeof(V)) = buf[u];
+    for (int u = 0; u < kMoveRows; ++u)
+      if (to[u] != ~0u) {
+        *reinterpret_cast<uint4*>(base + static_cast<uint64_t>(to[u]) * (MX ? 8 : 16)) = buf[u];
+        if (MX && x == 0) store_scales<SC>(scales + (to[u] >> 2), sc[u], packed);
       }
-    }
-  }
-}
-
-// grid (parts, H, S): parts = 2 (K, V), or 4 with the MXFP8 scales.
-__global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictParams A) {
-  grid_dependency_wait();
-  allow_dependent_launch();
-  const int part = blockIdx.x, h = blockIdx.y, i = blockIdx.z;
-  const SeqView s = seq_view(A.q, i, false);
-  if (!s.ok || s.ctx <= A.keep) return;
-  const int32_t* kept = A.kept + (static_cast<int64_t>(i) * A.H + h) * A.keep;
-  if (part < 2) {
-    uint8_t* base = part ? A.c.v : A.c.k;
-    const int bytes = A.mx ? A.D : 2 * A.D;
-    move_rows<uint4>(A, base, i, h, kept, A.keep, bytes / 16, 0, A.mx ? 1 : 2, 1);
-  } else {
-    uint8_t* base = part == 3 ? A.c.vs : A.c.ks;
-    move_rows<uint8_t>(A, base, i, h, kept, A.keep, A.D / 32, 0, 1, 32);
   }
 }
 

@@ -9,6 +9,7 @@ using TreeStepFn = void (*)(TreeStepParams);
 using AttendFn = void (*)(AttendParams);
 using JoinFn = void (*)(AttendParams, int, int, int);
 using AttendTcFn = void (*)(AttendParams, int, int);
+using MoveFn = void (*)(EvictParams);
 using WeighFn = void (*)(WeighParams);
 
 // nullptr for an unsupported combination.
@@ -28,8 +29,8 @@ AttendTc pick_attend_tc(int D, bool mx, int rows);
 JoinFn pick_attend_join(int D);
 WeighFn pick_weigh(int D, bool mx);
 void (*accept_fn())(AcceptParams);
-void (*evict_select_fn())(EvictParams);
-void (*evict_move_fn())(EvictParams);
+const void* evict_select_fn();  // (EvictParams, int room)
+MoveFn pick_evict_move(int D, bool mx);
 
 // Dynamic shared memory of attend_rows_kernel: Q, then the warps' results.
 inline size_t attend_rows_smem(int D, int nt) {

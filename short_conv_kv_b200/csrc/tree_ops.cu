@@ -26,6 +26,34 @@ bool aligned(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) &
 
 bool head_dim_ok(int D) { return D == 64 || D == 128 || D == 256; }
 
+// launch() with the grid's x dimension in clusters of c CTAs.
+int launch_clusters(const void* fn, dim3 grid, int c, int threads, size_t smem, void** args,
+                    void* stream) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = static_cast<cudaStream_t>(stream);
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = c;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  cudaError_t e = cudaLaunchKernelExC(&cfg, fn, args);
+  if (e == cudaSuccess) e = cudaGetLastError();
+  if (e != cudaSuccess) {
+    snprintf(g_cuda_error, sizeof g_cuda_error, "%s: %s", cudaGetErrorName(e),
+             cudaGetErrorString(e));
+    return SCONV_KV_ERR_CUDA;
+  }
+  g_cuda_error[0] = '\0';
+  return SCONV_KV_OK;
+}
+
 // Cache layout and paged sequences; the kernels keep a row's offset in 32
 // bits, in units of 8 elements.
 int check_paged(const sconv_kv_paged_t* seqs, const sconv_kv_cache_layout_t* layout, int H, int D,
@@ -60,7 +88,8 @@ int check_paged(const sconv_kv_paged_t* seqs, const sconv_kv_cache_layout_t* lay
   Q->lens = seqs->context_lens;
   Q->table = seqs->block_table;
   Q->table_stride = seqs->table_stride;
-  Q->capacity = seqs->table_width * layout->page_size;
+  // (kernels step up to 2^16 positions past the end)
+  Q->capacity = std::min<int64_t>(seqs->table_width * layout->page_size, INT32_MAX - 65536);
   Q->num_seqs = seqs->num_seqs;
   Q->num_pages = static_cast<int>(layout->num_pages);
   Q->page_size = static_cast<int>(layout->page_size);
@@ -103,7 +132,8 @@ CacheParts parts_of(const void* k, const void* v, const void* ks, const void* vs
                       layout->stride_page / 32 % row == 0;
   const bool words = layout->stride_slot / 32 % 4 == 0 && layout->stride_page / 32 % 4 == 0;
   auto raw = [](const void* p) { return const_cast<uint8_t*>(static_cast<const uint8_t*>(p)); };
-  return {raw(k), raw(v), raw(ks), raw(vs), packed ? 1 : 0, words ? 1 : 0};
+  return {raw(k), raw(v), raw(ks), raw(vs), packed ? 1 : 0,
+          packed && aligned(vs, static_cast<size_t>(row)) ? 1 : 0, words ? 1 : 0};
 }
 
 int check_heads(int HQ, int H, int64_t tok, int64_t head, int D) {
@@ -388,13 +418,31 @@ int evict_impl(const float* weights, int64_t positions, int64_t w_seq, int64_t w
   A.recent = recent;
   A.kept = kept;
   A.new_lens = new_lens;
+  // Clusters: as many CTAs a (sequence, head) as fill the GPU, while each has
+  // 2048 positions.  (16 sequences of 8 heads: 2 a selection, 1 a movement, 8 of either for
+  // a single sequence.)
+  const int64_t units = static_cast<int64_t>(H) * seqs->num_seqs;
+  auto spread = [&](int64_t n, int64_t per) {
+    int c = 1;
+    while (c < sconv::kMaxCluster && n * c < per * sm_count() && c * 2048ll < A.q.capacity) c *= 2;
+    return c;
+  };
+  {
+    const int c = spread(units, 1);
+    // a slice's keys, if they fit
+    const int64_t slice = (A.q.capacity / c + 1025) / 1024 * 1024 + 1024;
+    int room = static_cast<int>(std::min<int64_t>(slice, 48 * 1024));
+    const void* fn = sconv::evict_select_fn();
+    if (!smem_attr_set(fn, 4 * static_cast<size_t>(room))) return SCONV_KV_ERR_CUDA;
+    void* args[] = {&A, &room};
+    rc = launch_clusters(fn, dim3(H * c, seqs->num_seqs), c, sconv::kSelectThreads,
+                         4 * static_cast<size_t>(room), args, stream);
+    if (rc != SCONV_KV_OK) return rc;
+  }
+  const int c = spread(2 * units, 1);
   void* args[] = {&A};
-  rc = launch(reinterpret_cast<const void*>(sconv::evict_select_fn()),
-                          dim3(H, seqs->num_seqs), dim3(sconv::kSelectThreads), args, 0, stream);
-  if (rc != SCONV_KV_OK) return rc;
-  return launch(reinterpret_cast<const void*>(sconv::evict_move_fn()),
-                            dim3(mx ? 4 : 2, H, seqs->num_seqs), dim3(sconv::kMoveThreads), args, 0,
-                            stream);
+  return launch_clusters(reinterpret_cast<const void*>(sconv::pick_evict_move(D, mx)),
+                         dim3(2 * H * c, seqs->num_seqs), c, sconv::kMoveThreads, 0, args, stream);
 }
 
 }  // namespace

@@ -38,8 +38,9 @@ struct CacheParts {
   uint8_t* v;
   uint8_t* ks;
   uint8_t* vs;
-  int ks_packed;  // a row's D/32 K scales can be loaded at once (aligned)
-  int words;      // a head's scales begin at the same byte of a 4-byte word in every row
+  int ks_packed;      // a row's D/32 K scales can be loaded at once (aligned)
+  int scales_packed;  // the same of V's as well
+  int words;          // a head's scales begin at the same byte of a 4-byte word in every row
 };
 
 struct TreeStepParams {
@@ -106,7 +107,8 @@ struct WeighParams {
 };
 
 constexpr int kSelectThreads = 1024;
-constexpr int kMoveThreads = 256;
+constexpr int kMoveThreads = 512;
+constexpr int kMaxCluster = 8;
 
 struct EvictParams {
   PagedSeqs q;
