@@ -618,163 +618,27 @@ def unfused_step_noalloc(k, v, cu_seqlens, conv_w_k, conv_w_v, gamma_k, gamma_v,
 
 # ------------------------------------------- drafted trees, and the cache's eviction
 #
-# These calls run once per decode step and layer, so their marshalling reads
-# every tensor property once and builds nothing that the call does not need.
-
-_I32, _I64, _F32, _BF16, _U8 = torch.int32, torch.int64, torch.float32, torch.bfloat16, torch.uint8
+# These calls run once per decode step and layer: their arguments are checked and
+# passed on in compiled code (csrc/tree_bind.cpp).
 
 
-def _on(dev, stream, name, fn, *args):
-    """Call the C entry point with CUDA device `dev` current, on `stream` or the
-    device's current one."""
-    if dev < 0:
-        raise ValueError(f"{name}: the tensors must be on a CUDA device")
-    s = torch.cuda.current_stream(dev).cuda_stream if stream is None else _stream(stream)
-    if torch.cuda.current_device() == dev:
-        rc = fn(*args, s)
-    else:
-        with torch.cuda.device(dev):
-            rc = fn(*args, s)
-    if rc != OK:
-        raise SconvKVError(rc, name)
+def _load_tree():
+    if not os.path.exists(_build.TREE):
+        raise ImportError(f"{_build.TREE} is not built; run `python -m short_conv_kv_b200.build`")
+    from . import _tree as module
+    names = [n + m for n in ("tree_step", "tree_attention", "attention_weights", "tree_accept", "evict")
+             for m in ("", "_mxfp8")]
+    module.bind({"sconv_kv_" + n: ctypes.cast(getattr(_lib, "sconv_kv_" + n), ctypes.c_void_p).value
+                 for n in names})
+    return module
 
 
-def _dense(t, name, dtype, shape, dev):
-    """Pointer of a contiguous tensor, checked."""
-    if t.dtype is not dtype:
-        raise TypeError(f"{name} must be {str(dtype)[6:]}")
-    if t.shape != shape or not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous {list(shape)}, not {list(t.shape)}")
-    if t.get_device() != dev:
-        raise ValueError(f"{name} must be on device {dev}")
-    return t.data_ptr()
+_tree = _load_tree()
 
 
-def _flag(err_flag, dev):
-    return None if err_flag is None else _dense(err_flag, "err_flag", _I32, (1,), dev)
-
-
-def _paged(context_lens, block_table, dev, cu_draft=None, parents=None, num_tokens=0, max_draft=0):
-    if block_table.dtype is not _I32 or block_table.dim() != 2 or block_table.stride(1) != 1:
-        raise TypeError("block_table must be int32 [num_seqs, pages] with unit page stride")
-    if block_table.get_device() != dev:
-        raise ValueError(f"block_table must be on device {dev}")
-    S, width = block_table.shape
-    cu = par = None
-    if cu_draft is not None:
-        cu = _dense(cu_draft, "cu_draft", _I32, (S + 1,), dev)
-        par = _dense(parents, "parents", _I32, (num_tokens,), dev)
-    return S, Paged(cu, par, num_tokens, S, max_draft,
-                    _dense(context_lens, "context_lens", _I32, (S,), dev), block_table.data_ptr(),
-                    width, max(block_table.stride(0), width))
-
-
-def _cache(parts, dev):
-    """(layout, pointers) of a bf16 cache (K, V) or an MXFP8 one (K codes, K scales,
-    V codes, V scales); K's alone where that is all there is."""
-    k = parts[0]
-    shape, stride = k.shape, k.stride()
-    if len(shape) != 4 or stride[3] != 1:
-        raise ValueError("cache must be [num_pages, page_size, Hkv, D] with dim stride 1")
-    mx = k.dtype is _U8
-    ptrs = []
-    for n, t in enumerate(parts):
-        if t.get_device() != dev:
-            raise ValueError(f"the caches must be on device {dev}")
-        if mx and n & 1:
-            st = t.stride()
-            if t.dtype is not _U8 or t.shape != (*shape[:3], shape[3] // 32) or st[3] != 1 or \
-                    (st[0] * 32, st[1] * 32, st[2] * 32) != stride[:3]:
-                raise ValueError("scale caches must be uint8 [num_pages, page_size, Hkv, D/32] "
-                                 "with strides equal to the data strides / 32")
-        elif n:
-            if t.dtype is not k.dtype or t.shape != shape or t.stride() != stride:
-                raise ValueError("K and V caches must have the same type, shape and strides")
-        ptrs.append(t.data_ptr())
-    return CacheLayout(*shape, *stride[:3], 0), ptrs
-
-
-def _bf16_cache(parts, dev):
-    for t in parts:
-        if t.dtype is not _BF16:
-            raise TypeError("caches must be bfloat16")
-    return _cache(parts, dev)
-
-
-def _mx_cache(parts, dev):
-    if parts[0].dtype is not _U8:
-        raise TypeError("MXFP8 code caches must be uint8")
-    return _cache(parts, dev)
-
-
-def _heads(x, name, dev):
-    """(pointer, token stride, head stride) of bf16 [T, Hq, D] with unit dim stride."""
-    if x.dtype is not _BF16:
-        raise TypeError(f"{name} must be bfloat16")
-    if x.dim() != 3 or x.stride(2) != 1:
-        raise ValueError(f"{name} must be [T, Hq, D] with unit dim stride")
-    if x.get_device() != dev:
-        raise ValueError(f"{name} must be on device {dev}")
-    T, H, D = x.shape
-    st, sh, _ = x.stride()
-    # a dimension of size 1 has a stride of its own making
-    return x.data_ptr(), st if T > 1 else H * D, sh if H > 1 else D
-
-
-def _raw_rows(k, v, dev):
-    kp, rs = _rows(k, "k")
-    vp, rs_v = _rows(v, "v")
-    if rs != rs_v or v.shape != k.shape:
-        raise ValueError("k and v must share shape and row stride")
-    if v.get_device() != dev:
-        raise ValueError(f"v must be on device {dev}")
-    return kp, vp, rs
-
-
-def _weight_rows(weights, name, S, H, dev):
-    """(pointer, positions, sequence stride, head stride) of fp32 [S, Hkv, positions]."""
-    if weights.dtype is not _F32:
-        raise TypeError(f"{name} must be float32")
-    shape = weights.shape
-    if len(shape) != 3 or shape[0] != S or shape[1] != H or weights.stride(2) != 1:
-        raise ValueError(f"{name} must be [{S}, {H}, positions] with unit position stride")
-    if weights.get_device() != dev:
-        raise ValueError(f"{name} must be on device {dev}")
-    return weights.data_ptr(), shape[2], weights.stride(0), weights.stride(1)
-
-
-def _tree_step(name, fn, k, v, cu_draft, parents, conv_w_k, conv_w_v, gamma_k, gamma_v, eps,
-               conv_state, slot_mapping, cache, state_indices, state_positions, err_flag, stream):
-    dev = k.get_device()
-    kp, vp, rs = _raw_rows(k, v, dev)
-    lay, ptrs = cache
-    T, S = k.shape[0], cu_draft.shape[0] - 1
-    H, D = lay.num_kv_heads, lay.head_dim
-    W = conv_w_k.shape[0]
-    taps = (W, H * D)
-    gshape = (H, D) if gamma_k.dim() == 2 else (D,)
-    cu = _dense(cu_draft, "cu_draft", _I32, (S + 1,), dev)
-    par = _dense(parents, "parents", _I32, (T,), dev)
-    wk = _dense(conv_w_k, "conv_w_k", _BF16, taps, dev)
-    wv = _dense(conv_w_v, "conv_w_v", _BF16, taps, dev)
-    gk = _dense(gamma_k, "gamma_k", _F32, gshape, dev)
-    gv = _dense(gamma_v, "gamma_v", _F32, gshape, dev)
-    slots = _dense(slot_mapping, "slot_mapping", _I64, (T,), dev)
-    st, pool = _state(conv_state, W, H * D, dev)
-    si = None if state_indices is None else _dense(state_indices, "state_indices", _I32, (S,), dev)
-    if state_positions is not None:
-        _dense(state_positions, "state_positions", _I64, (S,), dev)
-    opts = _options(gamma_k, state_positions)
-    _on(dev, stream, name, fn, kp, vp, rs, T, cu, par, S, wk, wv, gk, gv, eps, W, H, D, st, si, pool,
-        slots, *ptrs, lay, opts, _flag(err_flag, dev))
-
-
-def _state(conv_state, W, C, dev):
-    """(pointer, rows) of the state pool; (None, 0) for W = 1, which has none."""
-    if W == 1:
-        return None, 0
-    pool = conv_state.shape[0]
-    return _dense(conv_state, "conv_state", _BF16, (pool, W - 1, 2 * C), dev), pool
+def _on(stream):
+    """A stream's handle; -1 for the current one of the tensors' device."""
+    return -1 if stream is None else _stream(stream)
 
 
 def tree_step(k, v, cu_draft, parents, conv_w_k, conv_w_v, gamma_k, gamma_v, eps, conv_state,
@@ -784,20 +648,22 @@ def tree_step(k, v, cu_draft, parents, conv_w_k, conv_w_v, gamma_k, gamma_v, eps
     window goes up its parents (int32 [T], local indices; -1 the context,
     <= -2 unused) and then into conv_state, which is only read.  cu_draft:
     int32 [S+1]; the rest as in prefill_varlen."""
-    _tree_step("sconv_kv_tree_step", _lib.sconv_kv_tree_step, k, v, cu_draft, parents, conv_w_k,
-               conv_w_v, gamma_k, gamma_v, eps, conv_state, slot_mapping,
-               _bf16_cache((k_cache, v_cache), k.get_device()), state_indices, state_positions,
-               err_flag, stream)
+    rc = _tree.tree_step(k, v, cu_draft, parents, conv_w_k, conv_w_v, gamma_k, gamma_v, eps, conv_state,
+                         slot_mapping, k_cache, None, v_cache, None, state_indices, err_flag, _on(stream),
+                         state_positions)
+    if rc:
+        raise SconvKVError(rc, "sconv_kv_tree_step")
 
 
 def tree_step_mxfp8(k, v, cu_draft, parents, conv_w_k, conv_w_v, gamma_k, gamma_v, eps, conv_state,
                     slot_mapping, k_data, k_scale, v_data, v_scale, state_indices=None,
                     err_flag=None, stream=None, state_positions=None):
     """tree_step with the MXFP8 cache store."""
-    _tree_step("sconv_kv_tree_step_mxfp8", _lib.sconv_kv_tree_step_mxfp8, k, v, cu_draft, parents,
-               conv_w_k, conv_w_v, gamma_k, gamma_v, eps, conv_state, slot_mapping,
-               _mx_cache((k_data, k_scale, v_data, v_scale), k.get_device()), state_indices,
-               state_positions, err_flag, stream)
+    rc = _tree.tree_step(k, v, cu_draft, parents, conv_w_k, conv_w_v, gamma_k, gamma_v, eps, conv_state,
+                         slot_mapping, k_data, k_scale, v_data, v_scale, state_indices, err_flag,
+                         _on(stream), state_positions)
+    if rc:
+        raise SconvKVError(rc, "sconv_kv_tree_step_mxfp8")
 
 
 def tree_attention_workspace(q, k_cache, num_seqs, max_draft):
@@ -813,30 +679,25 @@ def tree_attention_workspace(q, k_cache, num_seqs, max_draft):
         _check(_lib.sconv_kv_tree_attention_workspace(
             int(num_seqs), int(max_draft), q.shape[1], k_cache.shape[2], k_cache.shape[3],
             ctypes.byref(need)), "sconv_kv_tree_attention_workspace")
-    return torch.empty(need.value, dtype=_U8, device=q.device)
+    return torch.empty(need.value, dtype=torch.uint8, device=q.device)
 
 
-def _tree_attention(name, fn, q, cu_draft, parents, context_lens, block_table, k_cache, cache,
-                    scale, max_draft, out, lse, workspace, err_flag, stream):
-    dev = q.get_device()
-    lay, ptrs = cache
-    qp, qt, qh = _heads(q, "q", dev)
-    T, HQ, D = q.shape
-    if D != lay.head_dim:
-        raise ValueError("q and the cache differ in head_dim")
+def _tree_attention(name, q, cu_draft, parents, context_lens, block_table, kc, ks, vc, vs, scale,
+                    max_draft, out, lse, workspace, err_flag, stream):
     if out is None:
-        out = torch.empty((T, HQ, D), dtype=_BF16, device=q.device)
-    elif out.shape != q.shape:
-        raise ValueError("out must have q's shape")
-    op, ot, oh = _heads(out, "out", dev)
-    lp = None if lse is None else _dense(lse, "lse", _F32, (T, HQ), dev)
-    S, seqs = _paged(context_lens, block_table, dev, cu_draft, parents, T, max_draft)
-    if workspace is None:
-        workspace = tree_attention_workspace(q, k_cache, S, max_draft)
-    ws = _dense(workspace, "workspace", _U8, (workspace.numel(),), dev)
-    _on(dev, stream, name, fn, qp, qt, qh, HQ, lay.num_kv_heads, D, scale, seqs, *ptrs, lay, op, ot,
-        oh, lp, ws, workspace.numel(), _flag(err_flag, dev))
-    return out
+        out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+    while True:
+        rc = _tree.tree_attention(q, cu_draft, parents, context_lens, block_table, kc, ks, vc, vs, scale,
+                                  max_draft, out, lse, workspace, err_flag, _on(stream))
+        if rc == 0:
+            return out
+        if rc < 0:
+            raise SconvKVError(rc, name)
+        workspace = tree_attention_workspace(q, kc, block_table.shape[0], max_draft)
+        if stream is not None:  # it is freed on return, and may be in use there
+            other = stream if isinstance(stream, torch.cuda.Stream) else \
+                torch.cuda.ExternalStream(_stream(stream), device=q.device)
+            workspace.record_stream(other)
 
 
 def tree_attention(q, cu_draft, parents, context_lens, block_table, k_cache, v_cache, scale,
@@ -849,35 +710,18 @@ def tree_attention(q, cu_draft, parents, context_lens, block_table, k_cache, v_c
     (fp32 [T, Hq], natural logarithm) if given.  A chain of one token is the
     plain decode.  Pass a workspace (tree_attention_workspace) to allocate
     nothing, and under graph capture."""
-    return _tree_attention("sconv_kv_tree_attention", _lib.sconv_kv_tree_attention, q, cu_draft,
-                           parents, context_lens, block_table, k_cache,
-                           _bf16_cache((k_cache, v_cache), q.get_device()), scale, max_draft, out,
-                           lse, workspace, err_flag, stream)
+    return _tree_attention("sconv_kv_tree_attention", q, cu_draft, parents, context_lens, block_table,
+                           k_cache, None, v_cache, None, scale, max_draft, out, lse, workspace, err_flag,
+                           stream)
 
 
 def tree_attention_mxfp8(q, cu_draft, parents, context_lens, block_table, k_data, k_scale, v_data,
                          v_scale, scale, max_draft, out=None, lse=None, workspace=None,
                          err_flag=None, stream=None):
     """tree_attention over an MXFP8 cache."""
-    return _tree_attention("sconv_kv_tree_attention_mxfp8", _lib.sconv_kv_tree_attention_mxfp8, q,
-                           cu_draft, parents, context_lens, block_table, k_data,
-                           _mx_cache((k_data, k_scale, v_data, v_scale), q.get_device()), scale,
-                           max_draft, out, lse, workspace, err_flag, stream)
-
-
-def _attention_weights(name, fn, q, lse, cu_draft, parents, context_lens, block_table, cache, scale,
-                       max_draft, weights, err_flag, stream):
-    dev = q.get_device()
-    lay, ptrs = cache
-    qp, qt, qh = _heads(q, "q", dev)
-    T, HQ, D = q.shape
-    if D != lay.head_dim:
-        raise ValueError("q and the cache differ in head_dim")
-    lp = _dense(lse, "lse", _F32, (T, HQ), dev)
-    S, seqs = _paged(context_lens, block_table, dev, cu_draft, parents, T, max_draft)
-    H = lay.num_kv_heads
-    _on(dev, stream, name, fn, qp, qt, qh, HQ, H, D, scale, lp, seqs, *ptrs, lay,
-        *_weight_rows(weights, "weights", S, H, dev), _flag(err_flag, dev))
+    return _tree_attention("sconv_kv_tree_attention_mxfp8", q, cu_draft, parents, context_lens,
+                           block_table, k_data, k_scale, v_data, v_scale, scale, max_draft, out, lse,
+                           workspace, err_flag, stream)
 
 
 def attention_weights(q, lse, cu_draft, parents, context_lens, block_table, k_cache, scale,
@@ -886,38 +730,19 @@ def attention_weights(q, lse, cu_draft, parents, context_lens, block_table, k_ca
     attention gave every cached row: += for the context, = for the drafted
     tokens' own rows.  q, lse: the inputs and the result of tree_attention.
     Tokens whose parent is <= -2 count nothing."""
-    _attention_weights("sconv_kv_attention_weights", _lib.sconv_kv_attention_weights, q, lse,
-                       cu_draft, parents, context_lens, block_table,
-                       _bf16_cache((k_cache,), q.get_device()), scale, max_draft, weights,
-                       err_flag, stream)
+    rc = _tree.attention_weights(q, lse, cu_draft, parents, context_lens, block_table, k_cache, None, scale,
+                                 max_draft, weights, err_flag, _on(stream))
+    if rc:
+        raise SconvKVError(rc, "sconv_kv_attention_weights")
 
 
 def attention_weights_mxfp8(q, lse, cu_draft, parents, context_lens, block_table, k_data, k_scale,
                             scale, max_draft, weights, err_flag=None, stream=None):
     """attention_weights over an MXFP8 cache."""
-    _attention_weights("sconv_kv_attention_weights_mxfp8", _lib.sconv_kv_attention_weights_mxfp8, q,
-                       lse, cu_draft, parents, context_lens, block_table,
-                       _mx_cache((k_data, k_scale), q.get_device()), scale, max_draft, weights,
-                       err_flag, stream)
-
-
-def _tree_accept(name, fn, k, v, cu_draft, parents, leaves, context_lens, block_table, W,
-                 conv_state, cache, new_lens, weights, state_indices, state_positions, err_flag,
-                 stream):
-    dev = k.get_device()
-    kp, vp, rs = _raw_rows(k, v, dev)
-    lay, ptrs = cache
-    H, D = lay.num_kv_heads, lay.head_dim
-    S, seqs = _paged(context_lens, block_table, dev, cu_draft, parents, k.shape[0], MAX_DRAFT)
-    lv = _dense(leaves, "leaves", _I32, (S,), dev)
-    nl = _dense(new_lens, "new_lens", _I32, (S,), dev)
-    si = None if state_indices is None else _dense(state_indices, "state_indices", _I32, (S,), dev)
-    sp = None if state_positions is None else _dense(state_positions, "state_positions", _I64, (S,),
-                                                     dev)
-    st, pool = _state(conv_state, W, H * D, dev)
-    wargs = (None, 0, 0, 0) if weights is None else _weight_rows(weights, "weights", S, H, dev)
-    _on(dev, stream, name, fn, kp, vp, rs, seqs, lv, W, H, D, st, si, pool, sp, *ptrs, lay, *wargs,
-        nl, _flag(err_flag, dev))
+    rc = _tree.attention_weights(q, lse, cu_draft, parents, context_lens, block_table, k_data, k_scale,
+                                 scale, max_draft, weights, err_flag, _on(stream))
+    if rc:
+        raise SconvKVError(rc, "sconv_kv_attention_weights_mxfp8")
 
 
 def tree_accept(k, v, cu_draft, parents, leaves, context_lens, block_table, W, conv_state, k_cache,
@@ -928,35 +753,22 @@ def tree_accept(k, v, cu_draft, parents, leaves, context_lens, block_table, W, c
     the positions behind the context, conv_state takes its raw rows, and
     new_lens (int32 [S], not context_lens itself) gets the new lengths.  k,
     v: the raw rows that tree_step was given."""
-    _tree_accept("sconv_kv_tree_accept", _lib.sconv_kv_tree_accept, k, v, cu_draft, parents, leaves,
-                 context_lens, block_table, W, conv_state,
-                 _bf16_cache((k_cache, v_cache), k.get_device()), new_lens, weights, state_indices,
-                 state_positions, err_flag, stream)
+    rc = _tree.tree_accept(k, v, cu_draft, parents, leaves, context_lens, block_table, W, conv_state, k_cache,
+                           None, v_cache, None, new_lens, weights, state_indices, state_positions, err_flag,
+                           _on(stream))
+    if rc:
+        raise SconvKVError(rc, "sconv_kv_tree_accept")
 
 
 def tree_accept_mxfp8(k, v, cu_draft, parents, leaves, context_lens, block_table, W, conv_state,
                       k_data, k_scale, v_data, v_scale, new_lens, weights=None,
                       state_indices=None, state_positions=None, err_flag=None, stream=None):
     """tree_accept over an MXFP8 cache."""
-    _tree_accept("sconv_kv_tree_accept_mxfp8", _lib.sconv_kv_tree_accept_mxfp8, k, v, cu_draft,
-                 parents, leaves, context_lens, block_table, W, conv_state,
-                 _mx_cache((k_data, k_scale, v_data, v_scale), k.get_device()), new_lens, weights,
-                 state_indices, state_positions, err_flag, stream)
-
-
-def _evict(name, fn, weights, context_lens, block_table, cache, sinks, recent, kept, new_lens,
-           weights_out, err_flag, stream):
-    dev = weights.get_device()
-    lay, ptrs = cache
-    S, seqs = _paged(context_lens, block_table, dev)
-    H, keep = lay.num_kv_heads, kept.shape[-1]
-    kp = _dense(kept, "kept", _I32, (S, H, keep), dev)
-    nl = _dense(new_lens, "new_lens", _I32, (S,), dev)
-    wargs = _weight_rows(weights, "weights", S, H, dev)
-    oargs = (None, 0, 0, 0) if weights_out is None else _weight_rows(weights_out, "weights_out", S,
-                                                                     H, dev)
-    _on(dev, stream, name, fn, *wargs, seqs, keep, sinks, recent, H, lay.head_dim, *ptrs, lay, kp,
-        nl, *oargs, _flag(err_flag, dev))
+    rc = _tree.tree_accept(k, v, cu_draft, parents, leaves, context_lens, block_table, W, conv_state, k_data,
+                           k_scale, v_data, v_scale, new_lens, weights, state_indices, state_positions,
+                           err_flag, _on(stream))
+    if rc:
+        raise SconvKVError(rc, "sconv_kv_tree_accept_mxfp8")
 
 
 def evict(weights, context_lens, block_table, k_cache, v_cache, sinks, recent, kept, new_lens,
@@ -967,14 +779,16 @@ def evict(weights, context_lens, block_table, k_cache, v_cache, sinks, recent, k
     their order; kept (int32 [S, Hkv, keep]) gets their old positions (-1
     behind a shorter sequence), new_lens the lengths, weights_out (not
     weights itself) their weights."""
-    _evict("sconv_kv_evict", _lib.sconv_kv_evict, weights, context_lens, block_table,
-           _bf16_cache((k_cache, v_cache), weights.get_device()), sinks, recent, kept, new_lens,
-           weights_out, err_flag, stream)
+    rc = _tree.evict(weights, context_lens, block_table, k_cache, None, v_cache, None, sinks, recent, kept,
+                     new_lens, weights_out, err_flag, _on(stream))
+    if rc:
+        raise SconvKVError(rc, "sconv_kv_evict")
 
 
 def evict_mxfp8(weights, context_lens, block_table, k_data, k_scale, v_data, v_scale, sinks,
                 recent, kept, new_lens, weights_out=None, err_flag=None, stream=None):
     """evict over an MXFP8 cache."""
-    _evict("sconv_kv_evict_mxfp8", _lib.sconv_kv_evict_mxfp8, weights, context_lens, block_table,
-           _mx_cache((k_data, k_scale, v_data, v_scale), weights.get_device()), sinks, recent, kept,
-           new_lens, weights_out, err_flag, stream)
+    rc = _tree.evict(weights, context_lens, block_table, k_data, k_scale, v_data, v_scale, sinks, recent,
+                     kept, new_lens, weights_out, err_flag, _on(stream))
+    if rc:
+        raise SconvKVError(rc, "sconv_kv_evict_mxfp8")
