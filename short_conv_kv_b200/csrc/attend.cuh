@@ -327,30 +327,6 @@ __global__ void __launch_bounds__(32 * kRowsWarps, D == 256 ? 2 : NT == 1 ? 4 : 
     const int total = sv.ctx + sv.n;
     const int key1 = min(total, t1 * kRowsTile);
 
-    // ---- Q rows and ancestor masks
-    if (masked_seq != seq) {
-      ancestor_masks(P.s, sv, s_anc, s_ptr, t0 == 0 && unit == 0);
-      masked_seq = seq;
-    }
-    for (int x = tid; x < R * (D / 8); x += THREADS) {
-      const int r = x / (D / 8), d = (x - r * (D / 8)) * 8;
-      uint4 v = make_uint4(0, 0, 0, 0);
-      if (r < rows) {
-        const int tok = (row0 + r) / P.g, hg = row0 + r - tok * P.g;
-        v = ld_ro(P.q + (sv.a + tok) * P.q_tok + (h * P.g + hg) * P.q_head + d);
-      }
-      *reinterpret_cast<uint4*>(smem + r * L::kQPitch + d * 2) = v;
-    }
-    __syncthreads();
-    // this lane's rows lr and lr + 8: their tokens (-1: unused, or beyond the unit)
-    int tok_of[NT];
-#pragma unroll
-    for (int r = 0; r < NT; ++r) {
-      const int row = lr + 8 * r;
-      const int tok = row < rows ? (row0 + row) / P.g : -1;
-      tok_of[r] = tok >= 0 && ((s_anc[tok][tok >> 5] >> (tok & 31)) & 1u) ? tok : -1;
-    }
-
     const uint8_t* kb = P.c.k + h * P.s.stride_head * (MX ? 1 : 2);
     const uint8_t* vb = P.c.v + h * P.s.stride_head * (MX ? 1 : 2);
     const uint8_t* ksb = MX ? P.c.ks + (h * P.s.stride_head >> 5) : nullptr;
@@ -423,6 +399,30 @@ __global__ void __launch_bounds__(32 * kRowsWarps, D == 256 ? 2 : NT == 1 ? 4 : 
       load_v(off);
       off_next = off_at(base + step, page_next);
     }
+    // ---- Q rows and ancestor masks
+    if (masked_seq != seq) {
+      ancestor_masks(P.s, sv, s_anc, s_ptr, t0 == 0 && unit == 0);
+      masked_seq = seq;
+    }
+    for (int x = tid; x < R * (D / 8); x += THREADS) {
+      const int r = x / (D / 8), d = (x - r * (D / 8)) * 8;
+      uint4 v = make_uint4(0, 0, 0, 0);
+      if (r < rows) {
+        const int tok = (row0 + r) / P.g, hg = row0 + r - tok * P.g;
+        v = ld_ro(P.q + (sv.a + tok) * P.q_tok + (h * P.g + hg) * P.q_head + d);
+      }
+      *reinterpret_cast<uint4*>(smem + r * L::kQPitch + d * 2) = v;
+    }
+    __syncthreads();
+    // this lane's rows lr and lr + 8: their tokens (-1: unused, or beyond the unit)
+    int tok_of[NT];
+#pragma unroll
+    for (int r = 0; r < NT; ++r) {
+      const int row = lr + 8 * r;
+      const int tok = row < rows ? (row0 + row) / P.g : -1;
+      tok_of[r] = tok >= 0 && ((s_anc[tok][tok >> 5] >> (tok & 31)) & 1u) ? tok : -1;
+    }
+
     for (; base < key1; base += step) {
       const bool more = base + step < key1;
       if (more) page_next = page_at(base + 2 * step);
@@ -652,19 +652,26 @@ __global__ void __launch_bounds__(32 * kRowsWarps, D == 256 ? 2 : NT == 1 ? 4 : 
 
 // ------------------------------------------------------------------- the join
 //
-// grid (num_seqs * M-tiles, H, rows / 4): a warp a row.  A unit that one CTA
-// finished is skipped.
+// Few rows (split): grid (num_seqs * M-tiles, H, rows), a block a row, its four warps a
+// quarter of the parts each; there can be a part a CTA (8192 tokens, one
+// row: 74; 33 us a call with a warp a row, 24 so).  More rows: grid (.., rows / 4), a warp a
+// row, as its parts are few (32 ragged trees: 224 us with a block a row, 185 so).  A unit
+// that one CTA finished is skipped.
 template <int D>
 __global__ void __launch_bounds__(128) attend_join_kernel(const AttendParams P, int R, int tile,
-                                                          int mtiles) {
+                                                          int mtiles, int split) {
   grid_dependency_wait();
   allow_dependent_launch();
+  constexpr int V = D / 32;  // dims a lane
+  __shared__ float2 s_ml[4];
+  __shared__ float s_o[4][D];
   const int seq = blockIdx.x / mtiles, mt = blockIdx.x - seq * mtiles, h = blockIdx.y;
-  const int lane = threadIdx.x & 31;
-  const int r = blockIdx.z * 4 + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int r = split ? blockIdx.z : blockIdx.z * 4 + warp;
+  const int w0 = split ? warp : 0, ws = split ? 4 : 1;  // this warp's parts
   const SeqView sv = seq_view(P.s, seq, false);
   const SeqTiles st = seq_tiles(sv, P.g, P.H, R, tile);
-  if (mt >= st.mt || mt * R + r >= sv.n * P.g || r >= R) return;
+  if (mt >= st.mt || r >= R || mt * R + r >= sv.n * P.g) return;
   const int64_t total = P.prefix[P.s.num_seqs];
   const int64_t u0 = P.prefix[seq] + (static_cast<int64_t>(h) * st.mt + mt) * st.kt;
   const int parts = static_cast<int>(min(static_cast<int64_t>(P.parts), total));
@@ -672,17 +679,16 @@ __global__ void __launch_bounds__(128) attend_join_kernel(const AttendParams P, 
   if (c0 == c1) return;
   const int64_t first = 2 * static_cast<int64_t>(c0) + (range_start(c0, total, parts) == u0 ? 0 : 1);
   auto at = [&](int c) { return (c == c0 ? first : 2 * static_cast<int64_t>(c)) * R + r; };
-  // the maximum over the parts, a lane a part
+  // the maximum over this warp's parts, a lane a part
   float m = -INFINITY;
-  for (int c = c0 + lane; c <= c1; c += 32) m = fmaxf(m, P.part_ml[at(c)].x);
+  for (int c = c0 + w0 + ws * lane; c <= c1; c += 32 * ws) m = fmaxf(m, P.part_ml[at(c)].x);
 #pragma unroll
   for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(kFullMask, m, d));
-  constexpr int V = D / 32;  // dims a lane
   float acc[V], l = 0.f;
 #pragma unroll
   for (int e = 0; e < V; ++e) acc[e] = 0.f;
-#pragma unroll 4
-  for (int c = c0; c <= c1; ++c) {
+#pragma unroll 8
+  for (int c = c0 + w0; c <= c1; c += ws) {
     const int64_t a = at(c);
     const float2 ml = P.part_ml[a];
     const float f = merge_weight(ml.x, m);
@@ -707,13 +713,40 @@ __global__ void __launch_bounds__(128) attend_join_kernel(const AttendParams P, 
     for (int e = 0; e < V; ++e) acc[e] = none ? acc[e] : fmaf(v[e], f, acc[e]);
   }
   const int row = mt * R + r, tok = row / P.g, hq = h * P.g + row - tok * P.g;
-  const float inv = l == 0.f ? 0.f : 1.f / l;
-  uint16_t* to = P.out + (sv.a + tok) * P.o_tok + hq * P.o_head + lane * V;
+  uint16_t* to = P.out + (sv.a + tok) * P.o_tok + hq * P.o_head;
+  if (!split) {
+    const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
-  for (int e = 0; e < V; e += 2)
-    *reinterpret_cast<uint32_t*>(to + e) = pack_bf16x2(make_float2(acc[e] * inv, acc[e + 1] * inv));
-  if (lane == 0 && P.lse)
-    P.lse[(sv.a + tok) * P.HQ + hq] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+    for (int e = 0; e < V; e += 2)
+      *reinterpret_cast<uint32_t*>(to + lane * V + e) =
+          pack_bf16x2(make_float2(acc[e] * inv, acc[e + 1] * inv));
+    if (lane == 0 && P.lse)
+      P.lse[(sv.a + tok) * P.HQ + hq] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+    return;
+  }
+  if (lane == 0) s_ml[warp] = make_float2(m, l);
+#pragma unroll
+  for (int e = 0; e < V; ++e) s_o[warp][lane * V + e] = acc[e];
+  __syncthreads();
+  const float top = fmaxf(fmaxf(s_ml[0].x, s_ml[1].x), fmaxf(s_ml[2].x, s_ml[3].x));
+  float sum = 0.f, f[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const bool none = s_ml[k].x == -INFINITY && s_ml[k].y == 0.f;
+    f[k] = none ? 0.f : merge_weight(s_ml[k].x, top);
+    sum += none ? 0.f : s_ml[k].y * f[k];
+  }
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  for (int d = 2 * threadIdx.x; d < D; d += 256) {
+    float o[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+      o[e] = fmaf(s_o[3][d + e], f[3], fmaf(s_o[2][d + e], f[2],
+                  fmaf(s_o[1][d + e], f[1], s_o[0][d + e] * f[0])));
+    *reinterpret_cast<uint32_t*>(to + d) = pack_bf16x2(make_float2(o[0] * inv, o[1] * inv));
+  }
+  if (threadIdx.x == 0 && P.lse)
+    P.lse[(sv.a + tok) * P.HQ + hq] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
 }
 
 }  // namespace sconv

@@ -5,9 +5,9 @@
 
 namespace sconv {
 
-using TreeStepFn = void (*)(TreeStepParams);
+using TreeStepFn = void (*)(TreeStepParams, int);
 using AttendFn = void (*)(AttendParams);
-using JoinFn = void (*)(AttendParams, int, int, int);
+using JoinFn = void (*)(AttendParams, int, int, int, int);
 using AttendTcFn = void (*)(AttendParams, int, int);
 using MoveFn = void (*)(EvictParams);
 using WeighFn = void (*)(WeighParams);

@@ -241,10 +241,11 @@ int attention_impl(const void* q, int64_t q_tok, int64_t q_head, int HQ, int H, 
   int mtiles = (seqs->max_draft * P.g + A.rows - 1) / A.rows;
   const int64_t x = static_cast<int64_t>(seqs->num_seqs) * mtiles;
   if (x > INT32_MAX) return SCONV_KV_ERR_SHAPE;
-  void* args[] = {&P, &A.rows, &A.tile, &mtiles};
+  const int rows = std::min(A.rows, seqs->max_draft * P.g);
+  int split = rows <= 16;
+  void* args[] = {&P, &A.rows, &A.tile, &mtiles, &split};
   return launch(reinterpret_cast<const void*>(sconv::pick_attend_join(D)),
-                            dim3(static_cast<unsigned>(x), H, (A.rows + 3) / 4), dim3(128), args,
-                            0, stream);
+                dim3(static_cast<unsigned>(x), H, split ? rows : (rows + 3) / 4), dim3(128), args, 0, stream);
 }
 
 int weights_impl(const void* q, int64_t q_tok, int64_t q_head, int HQ, int H, int D, float scale,
@@ -315,12 +316,11 @@ int step_impl(const void* k, const void* v, int64_t row_stride, int64_t num_toke
   const bool lv = uses_layout_variants(options);
   const sconv::TreeStepFn fn = sconv::pick_tree_step(W, D, mx, lv);
   if (!fn) return SCONV_KV_ERR_UNSUPPORTED;
-  const int64_t blocks = (num_tokens * A.s.NG + 255) / 256;
-  const unsigned grid =
-      static_cast<unsigned>(std::min<int64_t>(blocks, 16ll * sm_count()));
-  void* args[] = {&A};
-  return launch(reinterpret_cast<const void*>(fn), dim3(grid), dim3(256), args, 0,
-                            stream);
+  // tokens a block: one while the blocks do not fill the GPU, up to eight
+  int tokens = static_cast<int>(std::clamp<int64_t>(num_tokens / (4 * sm_count()), 1, 8));
+  const unsigned grid = static_cast<unsigned>((num_tokens + tokens - 1) / tokens);
+  void* args[] = {&A, &tokens};
+  return launch(reinterpret_cast<const void*>(fn), dim3(grid), dim3(256), args, 0, stream);
 }
 
 int accept_impl(const void* k, const void* v, int64_t row_stride, const sconv_kv_paged_t* seqs,

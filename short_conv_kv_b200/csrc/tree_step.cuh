@@ -18,42 +18,41 @@
 
 namespace sconv {
 
-// One thread owns 8 channels of one token at a time; a warp's 32 groups are
-// consecutive, so a head's D/8 lanes are aligned.  idx runs in whole warps.
+// A block has up to kStepTokens tokens.  First a warp a token finds the token's
+// sequence, walks its parents and looks its slot up (some five dependent loads), then
+// all threads compute, 8 channels of one token at a time; a warp's 32 groups are
+// consecutive, so a head's D/8 lanes are aligned.  (With a token a block and the
+// walk in every thread, 8192 tokens took 53 us, all of it latency.)
+constexpr int kStepTokens = 8;
+
 template <int W, int D, bool MX, bool LV>
-__global__ void __launch_bounds__(256) tree_step_kernel(const TreeStepParams A) {
+__global__ void __launch_bounds__(256) tree_step_kernel(const TreeStepParams A, int tokens) {
   grid_dependency_wait();
   allow_dependent_launch();
   const StepParams& P = A.s;
-  const int64_t total = P.num_tokens * P.NG;
+  __shared__ int s_row[kStepTokens][8];  // tap j's row: a token, or ~q for row q of the state
+  __shared__ int64_t s_state[kStepTokens], s_off[kStepTokens];
+  __shared__ int s_run[kStepTokens];
   const int half = P.NG >> 1;
-  const int64_t warp_total = ((total + 31) / 32) * 32;
   const int64_t srow = 2 * static_cast<int64_t>(P.C);
-  for (int64_t idx = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x; idx < warp_total;
-       idx += static_cast<int64_t>(gridDim.x) * blockDim.x) {
-    const bool inside = idx < total;
-    const int64_t t = inside ? idx / P.NG : P.num_tokens - 1;
-    const int g = inside ? static_cast<int>(idx - t * P.NG) : 0;
-    // a warp spans several tokens only when a row has fewer than 32 groups
-    int i = 0;
-    {
-      int lo = 0, hi = P.num_seqs - 1;
-      while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (__ldg(P.cu_seqlens + mid) <= t) lo = mid; else hi = mid - 1;
-      }
-      i = lo;
-    }
-    const int64_t a = __ldg(P.cu_seqlens + i), e = __ldg(P.cu_seqlens + i + 1);
+  const int64_t t0 = blockIdx.x * static_cast<int64_t>(tokens);
+  const int here = static_cast<int>(min(static_cast<int64_t>(tokens), P.num_tokens - t0));
+  const int lane = threadIdx.x & 31, wp = threadIdx.x >> 5;
+  if (wp < here) {  // (a block has kStepTokens warps)
+    const int64_t t = t0 + wp;
     const int64_t slot = __ldg(P.slots + t);
-    bool run = inside && slot >= 0;
+    const int first_up = __ldg(A.parents + t);
+    const int i = warp_seq_of(P.cu_seqlens, P.num_seqs, t);
+    const int64_t a = __ldg(P.cu_seqlens + i), e = __ldg(P.cu_seqlens + i + 1);
+    int flags = 0;
+    bool run = slot >= 0;
     if (run && slot >= P.num_slots) {
-      raise_flag(P.err, kFlagSlotRange);
+      flags |= kFlagSlotRange;
       run = false;
     }
     if (!(a >= 0 && a <= t && t < e && e <= P.num_tokens)) {
       // behind the last sequence (t >= e) is not an error
-      if (inside && t < e) raise_flag(P.err, kFlagCuSeqlens);
+      if (t < e) flags |= kFlagCuSeqlens;
       run = false;
     }
     int64_t si = 0;
@@ -63,84 +62,114 @@ __global__ void __launch_bounds__(256) tree_step_kernel(const TreeStepParams A) 
       int64_t pos = 0;
       if (LV && P.state_pos) pos = __ldg(P.state_pos + i);
       if (si < 0 || si >= P.pool || pos < 0) {
-        raise_flag(P.err, kFlagStateIndex);
+        flags |= kFlagStateIndex;
         run = false;
       } else if (LV && P.state_pos) {
         rot = static_cast<int>(pos % (W > 1 ? W - 1 : 1));
       }
     }
-    // row of tap j: the ancestor W-1-j levels up, or a state row
-    const bool isv = g >= half;
-    const int c0 = (isv ? g - half : g) * 8;
-    const uint16_t* x = (isv ? P.v : P.k) + c0;
-    const uint16_t* st = P.state + si * (W - 1) * srow + (isv ? P.C : 0) + c0;
-    uint4 rows[W];
-    {
-      int64_t node = t - a;
-      int above = 0;  // state rows passed
+    // tap j's row: the ancestor W-1-j levels up, or a state row
+    int64_t node = t - a;
+    int above = 0;  // state rows passed
 #pragma unroll
-      for (int j = W - 1; j >= 0; --j) {
-        rows[j] = make_uint4(0, 0, 0, 0);
-        if (run) {
-          if (node >= 0) {
-            rows[j] = ld_ro(x + (a + node) * P.row_stride);
-            const int64_t up = __ldg(A.parents + a + node);
-            if (up < -1 || up >= node) {
-              // unused (the token itself below -1: padding), or malformed
-              if (up >= node || j != W - 1) raise_flag(P.err, kFlagTree);
-              run = false;
-            }
-            node = up;
-          } else {
-            int q = W - 2 - above;
-            if (LV) q = q + rot >= W - 1 ? q + rot - (W - 1) : q + rot;
-            rows[j] = *reinterpret_cast<const uint4*>(st + q * srow);
-            ++above;
-          }
+    for (int j = W - 1; j >= 0; --j) {
+      if (!run) break;
+      if (node >= 0) {
+        const int64_t up = j == W - 1 ? first_up : __ldg(A.parents + a + node);
+        if (lane == 0) s_row[wp][j] = static_cast<int>(a + node);
+        if (up < -1 || up >= node) {
+          // unused (the token itself below -1: padding), or malformed
+          if (up >= node || j != W - 1) flags |= kFlagTree;
+          run = false;
         }
+        node = up;
+      } else {
+        int q = W - 2 - above;
+        if (LV) q = q + rot >= W - 1 ? q + rot - (W - 1) : q + rot;
+        if (lane == 0) s_row[wp][j] = ~q;
+        ++above;
       }
     }
-    const uint16_t* w = (isv ? P.w_v : P.w_k) + c0;
-    float2 acc[4];
-#pragma unroll
-    for (int j = 0; j < W; ++j) {
-      float2 rf[4], tw[4];
-      unpack8(rows[j], rf);
-      unpack8(ld_ro(w + static_cast<int64_t>(j) * P.C), tw);
-#pragma unroll
-      for (int u = 0; u < 4; ++u) acc[u] = j == 0 ? fmul2(tw[u], rf[u]) : ffma2(tw[u], rf[u], acc[u]);
+    if (lane == 0) {
+      if (flags) raise_flag(P.err, flags);
+      int64_t off = 0;
+      if (run) {
+        const int64_t page = P.slot_linear ? 0 : slot / P.page_size;
+        off = page * P.stride_page + (slot - page * P.page_size) * P.stride_slot;
+      }
+      s_off[wp] = off;
+      s_state[wp] = si * (W - 1) * srow;
+      s_run[wp] = run;
     }
-    float2 s2 = fmul2(acc[0], acc[0]);
-    s2 = ffma2(acc[1], acc[1], s2);
-    s2 = ffma2(acc[2], acc[2], s2);
-    s2 = ffma2(acc[3], acc[3], s2);
-    const float ss = group_sum<D / 8>(s2.x + s2.y);
-    const float rn = rsqrt_approx(fmaf(ss, P.inv_d, P.eps));
+  }
+  __syncthreads();
+  // A thread keeps its 8 channels, taps and gammas unpacked in registers, and takes
+  // every side-th token (rows narrower than the block stand side by side).
+  const int side = max(1, 256 / P.NG), mine = threadIdx.x / P.NG;
+  for (int gb = 0; gb < P.NG; gb += 256) {
+    const int gg = P.NG < 256 ? static_cast<int>(threadIdx.x) - mine * P.NG : gb + static_cast<int>(threadIdx.x);
+    const bool inside = gg < P.NG && (P.NG >= 256 || mine < side);
+    const int g = inside ? gg : 0;
+    const bool isv = g >= half;
+    const int c0 = (isv ? g - half : g) * 8;
     const int d0 = c0 % D, h = c0 / D;
+    const uint16_t* x = (isv ? P.v : P.k) + c0;
+    const uint16_t* st0 = P.state + (isv ? P.C : 0) + c0;
+    const uint16_t* w = (isv ? P.w_v : P.w_k) + c0;
+    float2 tw[W][4];
+#pragma unroll
+    for (int j = 0; j < W; ++j) unpack8(ld_ro(w + static_cast<int64_t>(j) * P.C), tw[j]);
     const float* gam = (isv ? P.gamma_v : P.gamma_k) + h * P.gamma_hs + d0;
     const float4 ga = __ldg(reinterpret_cast<const float4*>(gam));
-    const float4 gb = __ldg(reinterpret_cast<const float4*>(gam) + 1);
+    const float4 gc = __ldg(reinterpret_cast<const float4*>(gam) + 1);
     const float2 gm[4] = {make_float2(ga.x, ga.y), make_float2(ga.z, ga.w),
-                          make_float2(gb.x, gb.y), make_float2(gb.z, gb.w)};
-    int64_t off = h * P.stride_head + d0;
-    if (run) {
-      const int64_t page = P.slot_linear ? 0 : slot / P.page_size;
-      off += page * P.stride_page + (slot - page * P.page_size) * P.stride_slot;
-    }
-    if constexpr (MX) {
-      // every lane takes part: the block scale is a 4-lane reduction
-      const float2 tt[4] = {fmul2(acc[0], gm[0]), fmul2(acc[1], gm[1]), fmul2(acc[2], gm[2]),
-                            fmul2(acc[3], gm[3])};
-      mx_store8(tt, rn, run, (isv ? P.v_data : P.k_data) + off,
-                (isv ? P.v_scale : P.k_scale) + (off >> 5));
-    } else if (run) {
-      const float2 rr = make_float2(rn, rn);
-      uint4 o;
-      o.x = pack_bf16x2(fmul2(fmul2(acc[0], rr), gm[0]));
-      o.y = pack_bf16x2(fmul2(fmul2(acc[1], rr), gm[1]));
-      o.z = pack_bf16x2(fmul2(fmul2(acc[2], rr), gm[2]));
-      o.w = pack_bf16x2(fmul2(fmul2(acc[3], rr), gm[3]));
-      *reinterpret_cast<uint4*>((isv ? P.v_cache : P.k_cache) + off) = o;
+                          make_float2(gc.x, gc.y), make_float2(gc.z, gc.w)};
+#pragma unroll 2
+    for (int k0 = 0; k0 < here; k0 += side) {
+      const int k = min(k0 + (P.NG < 256 ? mine : 0), kStepTokens - 1);
+      const bool run = inside && k < here && s_run[k];
+      const uint16_t* st = st0 + s_state[k];
+      uint4 rows[W];
+#pragma unroll
+      for (int j = 0; j < W; ++j) {
+        rows[j] = make_uint4(0, 0, 0, 0);
+        if (run) {
+          const int r = s_row[k][j];
+          rows[j] = r >= 0 ? ld_ro(x + r * P.row_stride)
+                           : *reinterpret_cast<const uint4*>(st + ~r * srow);
+        }
+      }
+      float2 acc[4];
+#pragma unroll
+      for (int j = 0; j < W; ++j) {
+        float2 rf[4];
+        unpack8(rows[j], rf);
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          acc[u] = j == 0 ? fmul2(tw[j][u], rf[u]) : ffma2(tw[j][u], rf[u], acc[u]);
+      }
+      float2 s2 = fmul2(acc[0], acc[0]);
+      s2 = ffma2(acc[1], acc[1], s2);
+      s2 = ffma2(acc[2], acc[2], s2);
+      s2 = ffma2(acc[3], acc[3], s2);
+      const float ss = group_sum<D / 8>(s2.x + s2.y);
+      const float rn = rsqrt_approx(fmaf(ss, P.inv_d, P.eps));
+      const int64_t off = s_off[k] + h * P.stride_head + d0;
+      if constexpr (MX) {
+        // every lane takes part: the block scale is a 4-lane reduction
+        const float2 tt[4] = {fmul2(acc[0], gm[0]), fmul2(acc[1], gm[1]), fmul2(acc[2], gm[2]),
+                              fmul2(acc[3], gm[3])};
+        mx_store8(tt, rn, run, (isv ? P.v_data : P.k_data) + off,
+                  (isv ? P.v_scale : P.k_scale) + (off >> 5));
+      } else if (run) {
+        const float2 rr = make_float2(rn, rn);
+        uint4 o;
+        o.x = pack_bf16x2(fmul2(fmul2(acc[0], rr), gm[0]));
+        o.y = pack_bf16x2(fmul2(fmul2(acc[1], rr), gm[1]));
+        o.z = pack_bf16x2(fmul2(fmul2(acc[2], rr), gm[2]));
+        o.w = pack_bf16x2(fmul2(fmul2(acc[3], rr), gm[3]));
+        *reinterpret_cast<uint4*>((isv ? P.v_cache : P.k_cache) + off) = o;
+      }
     }
   }
 }
