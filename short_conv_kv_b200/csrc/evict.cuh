@@ -101,7 +101,9 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const Evic
       cluster.sync();
       if (tid < 256) {
         uint32_t sum = 0;
-        for (int c = 0; c < ctas; ++c) sum += cluster.map_shared_rank(hist, c)[tid];
+#pragma unroll
+        for (int c = 0; c < kMaxCluster; ++c)  // all in flight at once
+          if (c < ctas) sum += cluster.map_shared_rank(hist, c)[tid];
         s_all[tid] = sum;
         s_hist[(step + 1) & 1][tid] = 0;  // last read before the sync above
       }
@@ -242,44 +244,56 @@ __global__ void __launch_bounds__(kMoveThreads, 2) evict_move_kernel(const Evict
   uint8_t* base = ((unit & 1) ? A.c.v : A.c.k) + head * (MX ? 1 : 2) + x * 16;
   uint8_t* scales = MX ? ((unit & 1) ? A.c.vs : A.c.ks) + (head >> 5) : nullptr;
   const bool packed = A.c.scales_packed;
-  auto offset = [&](int p) {  // ~0u for a page outside the cache
-    const int page = __ldg(table + page_index(A.q, p));
-    if (static_cast<unsigned>(page) >= static_cast<unsigned>(A.q.num_pages)) {
-      raise_flag(A.q.err, kFlagSlotRange);
-      return ~0u;
-    }
-    return row_off8(A.q, page, p);
-  };
-  for (int j0 = rank * kChunk; j0 - rank * kChunk < A.keep; j0 += ctas * kChunk) {
-    uint4 buf[kMoveRows];
-    SC sc[kMoveRows];
-    uint32_t to[kMoveRows];
-    int from[kMoveRows];
-#pragma unroll
-    for (int u = 0; u < kMoveRows; ++u) {
-      const int j = j0 + u * kSide + r;
-      from[u] = j < A.keep ? __ldg(kept + j) : -1;
-    }
-#pragma unroll
-    for (int u = 0; u < kMoveRows; ++u) {
-      const int j = j0 + u * kSide + r;
-      to[u] = ~0u;
-      if (from[u] > j) {
-        const uint32_t f = offset(from[u]);
-        if (f != ~0u) {
-          to[u] = offset(j);
-          buf[u] = *reinterpret_cast<const uint4*>(base + static_cast<uint64_t>(f) * (MX ? 8 : 16));
-          if (MX && x == 0) sc[u] = load_scales<SC>(scales + (f >> 2), packed);
+  // Where a round's rows are and go, looked up by a thread each while the
+  // round before is under way (~0u: stays, or a page outside the cache).
+  __shared__ uint32_t s_from[3][kChunk], s_to[3][kChunk];
+  auto look_up = [&](int b, int j0) {
+    for (int q = threadIdx.x; q < kChunk; q += kMoveThreads) {
+      const int j = j0 + q;
+      uint32_t f = ~0u, t = ~0u;
+      if (j < A.keep) {
+        const int p = __ldg(kept + j);
+        if (p > j) {
+          const int pf = __ldg(table + page_index(A.q, p)), pt = __ldg(table + page_index(A.q, j));
+          if (static_cast<unsigned>(pf) < static_cast<unsigned>(A.q.num_pages) &&
+              static_cast<unsigned>(pt) < static_cast<unsigned>(A.q.num_pages)) {
+            f = row_off8(A.q, pf, p);
+            t = row_off8(A.q, pt, j);
+          } else {
+            raise_flag(A.q.err, kFlagSlotRange);
+          }
         }
       }
+      s_from[b][q] = f;
+      s_to[b][q] = t;
     }
+  };
+  int j0 = rank * kChunk;
+  look_up(0, j0);
+  __syncthreads();
+  for (int b = 0; j0 - rank * kChunk < A.keep; j0 += ctas * kChunk) {
+    const int next = b == 2 ? 0 : b + 1;
+    uint4 buf[kMoveRows];
+    SC sc[kMoveRows];
+#pragma unroll
+    for (int u = 0; u < kMoveRows; ++u) {
+      const uint32_t f = s_from[b][u * kSide + r];
+      if (f != ~0u) {
+        buf[u] = *reinterpret_cast<const uint4*>(base + static_cast<uint64_t>(f) * (MX ? 8 : 16));
+        if (MX && x == 0) sc[u] = load_scales<SC>(scales + (f >> 2), packed);
+      }
+    }
+    look_up(next, j0 + ctas * kChunk);
     cluster.sync();
 #pragma unroll
-    for (int u = 0; u < kMoveRows; ++u)
-      if (to[u] != ~0u) {
-        *reinterpret_cast<uint4*>(base + static_cast<uint64_t>(to[u]) * (MX ? 8 : 16)) = buf[u];
-        if (MX && x == 0) store_scales<SC>(scales + (to[u] >> 2), sc[u], packed);
+    for (int u = 0; u < kMoveRows; ++u) {
+      const uint32_t t = s_to[b][u * kSide + r];
+      if (t != ~0u) {
+        *reinterpret_cast<uint4*>(base + static_cast<uint64_t>(t) * (MX ? 8 : 16)) = buf[u];
+        if (MX && x == 0) store_scales<SC>(scales + (t >> 2), sc[u], packed);
       }
+    }
+    b = next;  // (of three: one that a slower thread may still read is not written)
   }
 }
 

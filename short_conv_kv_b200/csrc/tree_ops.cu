@@ -395,7 +395,7 @@ int evict_impl(const float* weights, int64_t positions, int64_t w_seq, int64_t w
   memset(&A, 0, sizeof A);
   rc = check_paged(seqs, layout, H, D, false, mx, err, &A.q);
   if (rc != SCONV_KV_OK) return rc;
-  if (keep < 1 || sinks < 0 || recent < 0 || static_cast<int64_t>(sinks) + recent > keep ||
+  if (keep < 1 || keep > INT32_MAX - 65536 || sinks < 0 || recent < 0 || static_cast<int64_t>(sinks) + recent > keep ||
       positions < 0 || w_seq < 0 || w_head < 0 || seqs->num_seqs > 65535)
     return SCONV_KV_ERR_SHAPE;
   if (weights_out && (o_positions < std::min<int64_t>(keep, positions) || o_seq < 0 || o_head < 0))
