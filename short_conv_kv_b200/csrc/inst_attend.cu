@@ -28,8 +28,7 @@ WeighFn pick_weigh(int D, bool mx) {
   switch (D) {
     case 64: return mx ? &weigh_kernel<64, true> : &weigh_kernel<64, false>;
     case 128: return mx ? &weigh_kernel<128, true> : &weigh_kernel<128, false>;
-    case 256: return mx ? &weigh_kernel<256, true> : &weigh_kernel<256, false>;
-    default: return nullptr;
+    default: return mx ? &weigh_kernel<256, true> : &weigh_kernel<256, false>;
   }
 }
 

@@ -1,5 +1,7 @@
-// Instances of the attention kernel for many query rows.
+// Instances of the tensor-memory kernels: attention for many query rows, and the
+// attention weights.
 #include "attend_tc.cuh"
+#include "weigh_tc.cuh"
 #include "tree_instances.h"
 
 namespace sconv {
@@ -21,6 +23,25 @@ AttendTc tc_of(int rows) {
   A.units = room > 8 ? 8 : room;
   A.smem = static_cast<size_t>(fixed) + static_cast<size_t>(A.units) * F::kUnit;
   return A;
+}
+
+template <int D, bool MX>
+WeighTc weigh_tc_of(int rows) {
+  using F = FeedShape<D, 128, MX>;
+  WeighTc A;
+  A.fn = &weigh_tc_kernel<D, MX>;
+  A.threads = weigh_tc_threads<MX>();
+  A.rows = rows >= kWeighRows ? kWeighRows : (rows + 15) / 16 * 16;
+  const int fixed = (A.rows * D * 2 + 1023) / 1024 * 1024 + F::kRawBytes + 1024;
+  const int room = (227 * 1024 - 7168 - fixed) / F::kUnit;
+  A.units = room > 8 ? 8 : room;
+  A.smem = static_cast<size_t>(fixed) + static_cast<size_t>(A.units) * F::kUnit;
+  return A;
+}
+
+WeighTc pick_weigh_tc(int D, bool mx, int rows) {
+  if (D == 64) return mx ? weigh_tc_of<64, true>(rows) : weigh_tc_of<64, false>(rows);
+  return mx ? weigh_tc_of<128, true>(rows) : weigh_tc_of<128, false>(rows);
 }
 
 AttendTc pick_attend_tc(int D, bool mx, int rows) {

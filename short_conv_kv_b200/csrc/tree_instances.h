@@ -28,6 +28,16 @@ struct AttendTc {
 AttendTc pick_attend_tc(int D, bool mx, int rows);
 JoinFn pick_attend_join(int D);
 WeighFn pick_weigh(int D, bool mx);
+// weigh_tc_kernel (head_dim 64, 128; more than 16 rows) for up to `rows` query rows a K/V head: its threads, rows
+// a pass, units in the ring and dynamic shared memory.
+struct WeighTc {
+  void (*fn)(WeighParams, int, int);
+  int threads;
+  int rows;
+  int units;
+  size_t smem;
+};
+WeighTc pick_weigh_tc(int D, bool mx, int rows);
 void (*accept_fn())(AcceptParams);
 const void* evict_select_fn();  // (EvictParams, int room)
 MoveFn pick_evict_move(int D, bool mx);
@@ -36,6 +46,6 @@ MoveFn pick_evict_move(int D, bool mx);
 inline size_t attend_rows_smem(int D, int nt) {
   return static_cast<size_t>(kRowsWarps) * 8 * nt * (D + 4) * 4;
 }
-inline size_t weigh_smem(int D) { return static_cast<size_t>(D == 256 ? 64 : 128) * (2 * D + 64); }
+inline size_t weigh_smem(int D) { return static_cast<size_t>(D == 256 ? 64 : 16) * (2 * D + 64); }
 
 }  // namespace sconv

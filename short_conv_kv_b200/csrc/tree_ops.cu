@@ -279,15 +279,20 @@ int weights_impl(const void* q, int64_t q_tok, int64_t q_head, int HQ, int H, in
   W.weights = weights;
   W.w_seq = w_seq;
   W.w_head = w_head;
-  const sconv::WeighFn fn = sconv::pick_weigh(D, mx);
-  if (!fn) return SCONV_KV_ERR_UNSUPPORTED;
-  const size_t smem = sconv::weigh_smem(D);
-  const int threads = 32 * sconv::kWeighWarps;
-  const void* f = reinterpret_cast<const void*>(fn);
-  if (!smem_attr_set(f, smem)) return SCONV_KV_ERR_CUDA;
-  const int ctas = sm_count() * resident_per_sm(f, threads, smem, 2);
-  void* args[] = {&W};
-  return launch(f, dim3(ctas), dim3(threads), args, smem, stream);
+  if (D == 256 || seqs->max_draft * P.g <= 16) {  // both sides: weigh.cuh
+    const void* f = reinterpret_cast<const void*>(sconv::pick_weigh(D, mx));
+    const size_t smem = sconv::weigh_smem(D);
+    const int threads = 32 * sconv::kWeighWarps;
+    if (!smem_attr_set(f, smem)) return SCONV_KV_ERR_CUDA;
+    void* args[] = {&W};
+    return launch(f, dim3(sm_count() * resident_per_sm(f, threads, smem, 2)), dim3(threads), args,
+                  smem, stream);
+  }
+  sconv::WeighTc T = sconv::pick_weigh_tc(D, mx, seqs->max_draft * P.g);
+  const void* f = reinterpret_cast<const void*>(T.fn);
+  if (!smem_attr_set(f, T.smem)) return SCONV_KV_ERR_CUDA;
+  void* args[] = {&W, &T.rows, &T.units};
+  return launch(f, dim3(sm_count()), dim3(T.threads), args, T.smem, stream);
 }
 
 int step_impl(const void* k, const void* v, int64_t row_stride, int64_t num_tokens,
