@@ -22,11 +22,18 @@ namespace sconv {
 // sequence, walks its parents and looks its slot up (some five dependent loads), then
 // all threads compute, 8 channels of one token at a time; a warp's 32 groups are
 // consecutive, so a head's D/8 lanes are aligned.  (With a token a block and the
-// walk in every thread, 8192 tokens took 53 us, all of it latency.)
+// walk in every thread, 8192 tokens of 2 x 1024 channels took 53 us, so 33.)  Bound by
+// latency, so four blocks an SM go before loads ahead: with the next token's rows in
+// registers there are two, and it takes 40 us.
 constexpr int kStepTokens = 8;
 
+// (the raw rows and the state are only read)
+__device__ __forceinline__ uint4 ld_plain(const uint16_t* p) {
+  return *reinterpret_cast<const uint4*>(p);
+}
+
 template <int W, int D, bool MX, bool LV>
-__global__ void __launch_bounds__(256) tree_step_kernel(const TreeStepParams A, int tokens) {
+__global__ void __launch_bounds__(256, W <= 4 ? 4 : 2) tree_step_kernel(const TreeStepParams A, int tokens) {
   grid_dependency_wait();
   allow_dependent_launch();
   const StepParams& P = A.s;
@@ -124,21 +131,25 @@ __global__ void __launch_bounds__(256) tree_step_kernel(const TreeStepParams A, 
     const float4 gc = __ldg(reinterpret_cast<const float4*>(gam) + 1);
     const float2 gm[4] = {make_float2(ga.x, ga.y), make_float2(ga.z, ga.w),
                           make_float2(gc.x, gc.y), make_float2(gc.z, gc.w)};
-#pragma unroll 2
-    for (int k0 = 0; k0 < here; k0 += side) {
-      const int k = min(k0 + (P.NG < 256 ? mine : 0), kStepTokens - 1);
+    const int step0 = P.NG < 256 ? mine : 0;
+    // the rows of token k0 + step0, zeros where it does not run
+    auto load = [&](uint4(&rows)[W], int k0) {
+      const int k = min(k0 + step0, kStepTokens - 1);
       const bool run = inside && k < here && s_run[k];
       const uint16_t* st = st0 + s_state[k];
-      uint4 rows[W];
 #pragma unroll
       for (int j = 0; j < W; ++j) {
-        rows[j] = make_uint4(0, 0, 0, 0);
-        if (run) {
-          const int r = s_row[k][j];
-          rows[j] = r >= 0 ? ld_ro(x + r * P.row_stride)
-                           : *reinterpret_cast<const uint4*>(st + ~r * srow);
-        }
+        const int r = run ? s_row[k][j] : 0;
+        const uint16_t* from = r >= 0 ? x + r * P.row_stride : st + ~r * srow;
+        rows[j] = run ? ld_plain(from) : make_uint4(0, 0, 0, 0);
       }
+    };
+#pragma unroll 1
+    for (int k0 = 0; k0 < here; k0 += side) {
+      const int k = min(k0 + step0, kStepTokens - 1);
+      const bool run = inside && k < here && s_run[k];
+      uint4 rows[W];
+      load(rows, k0);
       float2 acc[4];
 #pragma unroll
       for (int j = 0; j < W; ++j) {
