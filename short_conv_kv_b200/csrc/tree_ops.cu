@@ -490,13 +490,16 @@ int sconv_kv_tree_attention_workspace(int num_seqs, int max_draft, int num_q_hea
       num_q_heads < num_kv_heads || num_q_heads % num_kv_heads || num_q_heads > (1 << 15) ||
       !head_dim_ok(head_dim))
     return SCONV_KV_ERR_SHAPE;
+  // enough for either store, and for calls with fewer drafted tokens, whose
+  // kernel and split may be others
   int64_t need = 0;
-  for (int mx = 0; mx < 2; ++mx) {  // enough for either store
-    AttendPlan A;
-    const int rc = plan_attend(max_draft, num_q_heads, num_kv_heads, head_dim, mx != 0, &A);
-    if (rc != SCONV_KV_OK) return rc;
-    need = std::max(need, workspace_need(num_seqs, head_dim, A.parts, A.rows));
-  }
+  for (int mx = 0; mx < 2; ++mx)
+    for (int n = 1; n <= max_draft; ++n) {
+      AttendPlan A;
+      const int rc = plan_attend(n, num_q_heads, num_kv_heads, head_dim, mx != 0, &A);
+      if (rc != SCONV_KV_OK) return rc;
+      need = std::max(need, workspace_need(num_seqs, head_dim, A.parts, A.rows));
+    }
   *bytes = need;
   return SCONV_KV_OK;
 }

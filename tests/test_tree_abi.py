@@ -277,3 +277,34 @@ def test_oracle_evict():
     assert ot.evict_pick(w, 8, 4, 1, 1) == [0, 1, 6, 7]
     assert ot.evict_pick(w, 8, 5, 0, 1) == [1, 2, 3, 6, 7]  # ties: the lower position
     assert ot.evict_pick(w, 3, 4, 1, 1) == [0, 1, 2]
+
+
+# ------------------------------------------------- rows that overlap in memory
+
+def test_binding_refuses_overlapping_rows():
+    """Broadcast inputs, whose stride the kernels could not follow, are refused (CPU
+    tensors: none reaches the library)."""
+    z, i32, bf = torch.zeros, torch.int32, torch.bfloat16
+    lens, cu, par = z(2, dtype=i32), z(3, dtype=i32), z(3, dtype=i32)
+    kc, table = z(8, 16, 2, 64, dtype=bf), z(2, 4, dtype=i32)
+    q, w, raw = z(3, 4, 64, dtype=bf), z(2, 2, 64), z(3, 128, dtype=bf)
+
+    def refused(fn, **kw):
+        with pytest.raises(ValueError, match="overlap"):
+            fn(**kw)
+    at = dict(cu_draft=cu, parents=par, context_lens=lens, k_cache=kc, scale=1.0, max_draft=2)
+    refused(b.tree_attention, q=q, v_cache=kc, block_table=table[:1].expand(2, 4), **at)
+    refused(b.attention_weights, q=q, lse=z(3, 4), block_table=table, weights=w[:1].expand(2, 2, 64), **at)
+    refused(b.attention_weights, q=q, lse=z(3, 4), block_table=table, weights=w[:, :1].expand(2, 2, 64), **at)
+    refused(b.evict, weights=w[:1].expand(2, 2, 64), context_lens=lens, block_table=table, k_cache=kc,
+            v_cache=kc, sinks=1, recent=1, kept=z(2, 2, 9, dtype=i32), new_lens=lens.clone())
+    one = raw[:1].expand(3, 128)
+    refused(b.tree_accept, k=one, v=one, cu_draft=cu, parents=par, leaves=lens, context_lens=lens,
+            block_table=table, W=1, conv_state=None, k_cache=kc, v_cache=kc, new_lens=lens.clone())
+    refused(b.tree_step, k=one, v=one, cu_draft=cu, parents=par, conv_w_k=z(1, 128, dtype=bf),
+            conv_w_v=z(1, 128, dtype=bf), gamma_k=z(64), gamma_v=z(64), eps=1e-6, conv_state=None,
+            slot_mapping=z(3, dtype=torch.int64), k_cache=kc, v_cache=kc)
+
+
+def test_evict_keep_limit():
+    assert evict(keep=2 ** 31 - 65536) == b.ERR_SHAPE
