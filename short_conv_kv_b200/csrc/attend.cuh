@@ -102,55 +102,77 @@ __device__ __forceinline__ float cache_value(const uint8_t* base, const uint8_t*
   }
 }
 
-// Tiles of one sequence: M-tiles, key tiles of one unit, and their product over
-// the K/V heads.
+// Tiles of one sequence: M-tiles, key tiles of one unit, and what all its units take of the
+// line over the K/V heads, where `extra` steps stand for a unit's beginning and end.
 struct SeqTiles {
   int mt;
   int kt;
   int64_t all;
 };
-__device__ __forceinline__ SeqTiles seq_tiles(const SeqView& s, int g, int H, int rows, int tile) {
+__device__ __forceinline__ SeqTiles seq_tiles(const SeqView& s, int g, int H, int rows, int tile,
+                                              int extra = 0) {
   SeqTiles t;
   t.mt = (s.n * g + rows - 1) / rows;
   t.kt = s.n ? static_cast<int>((static_cast<int64_t>(s.ctx) + s.n + tile - 1) / tile) : 0;
-  t.all = static_cast<int64_t>(t.mt) * H * t.kt;
+  t.all = t.kt ? static_cast<int64_t>(t.mt) * H * (t.kt + extra) : 0;
   return t;
 }
 
-// Where in the line of all tiles this CTA's range begins: the total, the
-// sequence that holds tile `first`, and the tiles before that sequence.  The first
-// CTA writes the prefix that the join reads (if there is one), and raises the flags.  Every
-// thread of the block takes part (THREADS of them); s_scan has THREADS/32 + 1
-// entries.
+// Where in the line of all tiles this CTA's range begins: the
+// sequence that holds step `first`, and the steps before that sequence.  The first
+// CTA writes the prefix that the join reads (if there is one; `extra` behind it), and raises
+// the flags.  `extra` comes in as what a unit's beginning and end cost, in tiles, and goes out
+// as 0 where a range is too short for it to matter: a range of more than `extra` steps
+// has a tile, which the join counts on.  Every thread of the block takes part (THREADS
+// of them); s_scan has 2 * THREADS/32 entries.
 template <int THREADS>
 __device__ __forceinline__ void find_range(const PagedSeqs& Q, int g, int H, int rows, int tile,
                                            int64_t* prefix, int part, int parts, int64_t* s_scan,
                                            int64_t* s_found, int64_t& first, int64_t& last,
-                                           int& seq, int64_t& seq_first) {
+                                           int& seq, int64_t& seq_first, int& extra) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  constexpr int kWarps = THREADS / 32;
   const int S = Q.num_seqs;
   const int per = (S + THREADS - 1) / THREADS;
   const int i0 = min(S, tid * per), i1 = min(S, i0 + per);
   const bool lead = part == 0;
-  int64_t sum = 0;
-  for (int i = i0; i < i1; ++i) sum += seq_tiles(seq_view(Q, i, lead), g, H, rows, tile).all;
-  int64_t inc = sum;
+  int64_t sum = 0, units = 0;
+  for (int i = i0; i < i1; ++i) {
+    const SeqTiles t = seq_tiles(seq_view(Q, i, lead), g, H, rows, tile);
+    sum += t.all;
+    units += t.kt ? static_cast<int64_t>(t.mt) * H : 0;
+  }
+  int64_t inc = sum, inu = units;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
-    const int64_t up = __shfl_up_sync(kFullMask, inc, d);
-    if (lane >= d) inc += up;
+    const int64_t up = __shfl_up_sync(kFullMask, inc, d), uu = __shfl_up_sync(kFullMask, inu, d);
+    if (lane >= d) {
+      inc += up;
+      inu += uu;
+    }
   }
-  if (lane == 31) s_scan[warp] = inc;
+  if (lane == 31) {
+    s_scan[warp] = inc;
+    s_scan[kWarps + warp] = inu;
+  }
   if (tid == 0) {
     s_found[0] = -1;
     s_found[1] = 0;
   }
   __syncthreads();
-  int64_t before = inc - sum, total = 0;
-  for (int k = 0; k < THREADS / 32; ++k) {
-    if (k < warp) before += s_scan[k];
+  int64_t before = inc - sum, total = 0, units_before = inu - units, units_all = 0;
+  for (int k = 0; k < kWarps; ++k) {
+    if (k < warp) {
+      before += s_scan[k];
+      units_before += s_scan[kWarps + k];
+    }
     total += s_scan[k];
+    units_all += s_scan[kWarps + k];
   }
+  if (total < 2ll * (extra + 1) * parts) extra = 0;
+  before += extra * units_before;
+  total += extra * units_all;
+  sum += extra * units;
   // no empty range between two others: the join counts on it
   const int64_t used = min(static_cast<int64_t>(parts), max(total, static_cast<int64_t>(1)));
   first = min(part, static_cast<int>(used)) * total / used;
@@ -158,7 +180,7 @@ __device__ __forceinline__ void find_range(const PagedSeqs& Q, int g, int H, int
   if (lead || (before <= first && first < before + sum)) {
     int64_t at = before;
     for (int i = i0; i < i1; ++i) {
-      const int64_t all = seq_tiles(seq_view(Q, i, false), g, H, rows, tile).all;
+      const int64_t all = seq_tiles(seq_view(Q, i, false), g, H, rows, tile, extra).all;
       if (lead && prefix) prefix[i] = at;
       if (at <= first && first < at + all) {
         s_found[0] = i;
@@ -166,7 +188,10 @@ __device__ __forceinline__ void find_range(const PagedSeqs& Q, int g, int H, int
       }
       at += all;
     }
-    if (lead && prefix && tid == THREADS - 1) prefix[S] = total;
+    if (lead && prefix && tid == THREADS - 1) {
+      prefix[S] = total;
+      prefix[S + 1] = extra;
+    }
   }
   __syncthreads();
   seq = static_cast<int>(s_found[0]);
@@ -297,15 +322,15 @@ __global__ void __launch_bounds__(32 * kRowsWarps, D == 256 ? 2 : NT == 1 ? 4 : 
   __shared__ uint32_t s_anc[kMaxDraft][kMaskWords];
   __shared__ int s_ptr[kMaxDraft];
   __shared__ float2 s_ml[kRowsWarps][R];
-  __shared__ int64_t s_scan[THREADS / 32], s_found[2];
+  __shared__ int64_t s_scan[2 * (THREADS / 32)], s_found[2];
   __shared__ int s_bad;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int lr = lane >> 2, lc = lane & 3;  // row (or key) and column of a fragment
 
   int64_t cur, end, seq_first;
-  int seq;
+  int seq, extra = 0;
   find_range<THREADS>(P.s, P.g, P.H, R, kRowsTile, P.prefix, blockIdx.x, gridDim.x, s_scan,
-                      s_found, cur, end, seq, seq_first);
+                      s_found, cur, end, seq, seq_first, extra);
   if (tid == 0) s_bad = 0;
   if (cur >= end) return;
   int segment = 0, masked_seq = -1;
@@ -673,11 +698,14 @@ __global__ void __launch_bounds__(128) attend_join_kernel(const AttendParams P, 
   const SeqTiles st = seq_tiles(sv, P.g, P.H, R, tile);
   if (mt >= st.mt || r >= R || mt * R + r >= sv.n * P.g) return;
   const int64_t total = P.prefix[P.s.num_seqs];
-  const int64_t u0 = P.prefix[seq] + (static_cast<int64_t>(h) * st.mt + mt) * st.kt;
+  const int extra = static_cast<int>(P.prefix[P.s.num_seqs + 1]);
+  // the unit's first step, and its first tile's
+  const int64_t u0 = P.prefix[seq] + (static_cast<int64_t>(h) * st.mt + mt) * (st.kt + extra);
+  const int64_t t0 = u0 + extra;
   const int parts = static_cast<int>(min(static_cast<int64_t>(P.parts), total));
-  const int c0 = range_of(u0, total, parts), c1 = range_of(u0 + st.kt - 1, total, parts);
+  const int c0 = range_of(t0, total, parts), c1 = range_of(t0 + st.kt - 1, total, parts);
   if (c0 == c1) return;
-  const int64_t first = 2 * static_cast<int64_t>(c0) + (range_start(c0, total, parts) == u0 ? 0 : 1);
+  const int64_t first = 2 * static_cast<int64_t>(c0) + (range_start(c0, total, parts) >= u0 ? 0 : 1);
   auto at = [&](int c) { return (c == c0 ? first : 2 * static_cast<int64_t>(c)) * R + r; };
   // the maximum over this warp's parts, a lane a part
   float m = -INFINITY;

@@ -43,6 +43,11 @@ __device__ __forceinline__ void fewer_registers() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
+// A unit's beginning and end (masks, queries, the first copies, the output), in tiles: a
+// range with many short contexts gets fewer of their tiles (32 ragged ones: 179 us
+// without).
+constexpr int kUnitExtra = 5;
+
 // Bits a0 .. a0+31 of the row's view of the keys behind the context: a < 0
 // (context) is seen, a draft where its bit is set.
 __device__ __forceinline__ uint32_t seen32(const uint32_t* anc, int a0, bool used) {
@@ -69,7 +74,7 @@ __global__ void __launch_bounds__(tc_threads<D, MX>(), 1)
   __shared__ uint32_t s_anc[kMaxDraft][kMaskWords];
   __shared__ int s_ptr[kMaxDraft];
   __shared__ float2 s_ml[2][128];
-  __shared__ int64_t s_scan[THREADS / 32], s_found[2];
+  __shared__ int64_t s_scan[2 * (THREADS / 32)], s_found[2];
   __shared__ uint64_t s_full[8], s_empty[8], s_score[2], s_prob[2], s_out[2], s_query, s_drain;
   __shared__ uint64_t s_raw_full[F::kRaw], s_raw_empty[F::kRaw];
   __shared__ uint32_t s_tmem;
@@ -102,9 +107,9 @@ __global__ void __launch_bounds__(tc_threads<D, MX>(), 1)
   if (warp == 0) tmem_alloc(&s_tmem, 512);
   tc_fence_before();
   int64_t cur, end, seq_first;
-  int seq;
+  int seq, extra = kUnitExtra;
   find_range<THREADS>(P.s, P.g, P.H, rows_unit, TN, P.prefix, blockIdx.x, gridDim.x, s_scan,
-                      s_found, cur, end, seq, seq_first);  // barriers inside
+                      s_found, cur, end, seq, seq_first, extra);  // barriers inside
   tc_fence_after();
   const uint32_t tmem = s_tmem;
 
@@ -115,23 +120,31 @@ __global__ void __launch_bounds__(tc_threads<D, MX>(), 1)
   bool pair = false;
   auto enter = [&] {
     sv = seq_view(P.s, seq, false);
-    st = seq_tiles(sv, P.g, P.H, rows_unit, TN);
+    st = seq_tiles(sv, P.g, P.H, rows_unit, TN, extra);
   };
-  auto locate = [&] {
-    while (cur >= seq_first + st.all) {  // the next sequence with tiles
-      seq_first += st.all;
-      ++seq;
-      enter();
-    }
-    const int64_t rel = cur - seq_first;
-    const int unit = static_cast<int>(rel / st.kt);
-    t0 = static_cast<int>(rel - static_cast<int64_t>(unit) * st.kt);
-    tiles = static_cast<int>(min(static_cast<int64_t>(st.kt - t0), end - cur));
-    h = unit / st.mt;
-    row0 = (unit - h * st.mt) * rows_unit;
+  auto locate = [&]() -> bool {  // false behind the last one
+    do {
+      if (cur >= end) return false;
+      while (cur >= seq_first + st.all) {  // the next sequence with tiles
+        seq_first += st.all;
+        ++seq;
+        enter();
+      }
+      const int64_t rel = cur - seq_first;
+      const int steps = st.kt + extra;
+      const int unit = static_cast<int>(rel / steps);
+      const int s0 = static_cast<int>(rel - static_cast<int64_t>(unit) * steps);
+      const int s1 = static_cast<int>(min(static_cast<int64_t>(steps), s0 + (end - cur)));
+      t0 = max(0, s0 - extra);
+      tiles = max(0, s1 - extra) - t0;
+      h = unit / st.mt;
+      row0 = (unit - h * st.mt) * rows_unit;
+      cur += s1 - s0;
+    } while (tiles == 0);
     rows = min(rows_unit, sv.n * P.g - row0);
     total = sv.ctx + sv.n;
     pair = NS == 2 && rows > 128;
+    return true;
   };
   if (cur < end) enter();
 
@@ -152,12 +165,7 @@ __global__ void __launch_bounds__(tc_threads<D, MX>(), 1)
       ok = __all_sync(kFullMask, ok);
     };
     auto meet = [&] { asm volatile("bar.sync 1, %0;" ::"n"(kSoft) : "memory"); };
-    while (cur < end) {
-      locate();
-      if (masked_seq != seq) {
-        ancestor_masks(P.s, sv, s_anc, s_ptr, t0 == 0 && h == 0 && row0 == 0, meet);
-        masked_seq = seq;
-      }
+    while (locate()) {
       // ---- Q, rows of both streams
       // (a thread keeps its 8 columns; the loads of eight rows are in flight at once)
       {
@@ -191,6 +199,11 @@ __global__ void __launch_bounds__(tc_threads<D, MX>(), 1)
       }
       async_proxy_fence();
       mbar_arrive(&s_query);
+      // the masks meanwhile: the first product does not need them
+      if (masked_seq != seq) {
+        ancestor_masks(P.s, sv, s_anc, s_ptr, t0 == 0 && h == 0 && row0 == 0, meet);
+        masked_seq = seq;
+      }
 
       const int mine = pair ? stream * 128 + r : r;  // row of the unit
       const int tok = mine < rows ? (row0 + mine) / P.g : 0;
@@ -394,7 +407,6 @@ __global__ void __launch_bounds__(tc_threads<D, MX>(), 1)
       }
       tc_fence_before();
       meet();  // Q, the masks, O and s_ml are free
-      cur += tiles;
       ++segment;
     }
     if (!ok && lane == 0) raise_flag(P.s.err, kFlagTimeout);
@@ -405,8 +417,7 @@ __global__ void __launch_bounds__(tc_threads<D, MX>(), 1)
     FeedRing R{units, s_full, s_empty, s_abort, ring_units};
     if constexpr (MX) {
       FeedRing Raw{raw, s_raw_full, s_raw_empty, s_abort, F::kRaw};
-      while (cur < end) {
-        locate();
+      while (locate()) {
         const int64_t head = h * P.s.stride_head >> 5;
         const int k_low = P.c.words ? reinterpret_cast<uintptr_t>(P.c.ks + head) & 3 : 0;
         const int v_low = P.c.words ? reinterpret_cast<uintptr_t>(P.c.vs + head) & 3 : 0;
@@ -418,11 +429,9 @@ __global__ void __launch_bounds__(tc_threads<D, MX>(), 1)
           const int clean = is_v ? max(0, min(TN, sv.ctx - (t0 + t) * TN)) : TN;
           FeedMx<D, TN>::decode(R, Raw, w, lane, is_v ? v_low : k_low, clean);
         }
-        cur += tiles;
       }
     } else {
-      while (cur < end) {
-        locate();
+      while (locate()) {
         const int64_t head = h * P.s.stride_head;
         const uint8_t *kb = P.c.k + head * 2, *vb = P.c.v + head * 2;
         const int32_t* table = P.s.table + seq * P.s.table_stride;
@@ -445,7 +454,6 @@ __global__ void __launch_bounds__(tc_threads<D, MX>(), 1)
           }
           FeedBf16<D, TN>::bring(R, w, lane, is_v ? vb : kb, t & 1 ? off1 : off0, clean);
         }
-        cur += tiles;
       }
       cp_commit();
       cp_wait<0>();
@@ -510,8 +518,7 @@ __global__ void __launch_bounds__(tc_threads<D, MX>(), 1)
       commit(&s_empty[slot]);
       next();
     };
-    while (cur < end && ok) {
-      locate();
+    while (ok && locate()) {
       wait(&s_query, queries++);
       if (pair) {
         unit(slot, phase);
@@ -567,7 +574,6 @@ __global__ void __launch_bounds__(tc_threads<D, MX>(), 1)
           }
         }
       }
-      cur += tiles;
     }
     // products still under way would write to freed tensor memory
     if (elect_one()) tc_commit(&s_drain);
@@ -580,8 +586,7 @@ __global__ void __launch_bounds__(tc_threads<D, MX>(), 1)
       using M = FeedMx<D, TN>;
       const int w = warp - (T::kSoftWarps + F::kWarps + 1);
       FeedRing Raw{raw, s_raw_full, s_raw_empty, s_abort, F::kRaw};
-      while (cur < end) {
-        locate();
+      while (locate()) {
         const int64_t head = h * P.s.stride_head;
         const int32_t* table = P.s.table + seq * P.s.table_stride;
         const int key0 = t0 * TN + w * 8 + (lane >> 2);
@@ -616,7 +621,6 @@ __global__ void __launch_bounds__(tc_threads<D, MX>(), 1)
           M::fetch(Raw, w, lane, (v ? P.c.v : P.c.k) + head, (v ? P.c.vs : P.c.ks) + (head >> 5),
                    P.c.words, off, total - (t0 + t) * TN);
         }
-        cur += tiles;
       }
       cp_commit();
       cp_wait<0>();

@@ -185,7 +185,7 @@ int plan_attend(int max_draft, int HQ, int H, int D, bool mx, AttendPlan* A) {
 // Workspace: prefix, then partial (m, l), then partial o.
 int64_t round256(int64_t x) { return (x + 255) / 256 * 256; }
 int64_t workspace_need(int num_seqs, int D, int parts, int rows) {
-  return round256(8 * (static_cast<int64_t>(num_seqs) + 1)) +
+  return round256(8 * (static_cast<int64_t>(num_seqs) + 2)) +
          round256(2ll * parts * rows * 8) + round256(2ll * parts * rows * D * 4);
 }
 
@@ -228,7 +228,7 @@ int attention_impl(const void* q, int64_t q_tok, int64_t q_head, int HQ, int H, 
   P.scale_log2 = scale * sconv::kLog2e;
   uint8_t* w = static_cast<uint8_t*>(workspace);
   P.prefix = reinterpret_cast<int64_t*>(w);
-  w += round256(8 * (static_cast<int64_t>(seqs->num_seqs) + 1));
+  w += round256(8 * (static_cast<int64_t>(seqs->num_seqs) + 2));
   P.part_ml = reinterpret_cast<float2*>(w);
   w += round256(2ll * A.parts * A.rows * 8);
   P.part_o = reinterpret_cast<float*>(w);

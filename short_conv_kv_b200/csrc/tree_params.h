@@ -89,7 +89,7 @@ struct AttendParams {
   int H;
   int g;
   float scale_log2;  // scale * log2(e)
-  // workspace: tile prefix of the sequences [num_seqs + 1], then per CTA two
+  // workspace: step prefix of the sequences [num_seqs + 2], then per CTA two
   // partial results of R rows: o (fp32 [R, D]) and (m, l)
   int64_t* prefix;
   float* part_o;

@@ -34,13 +34,13 @@ __global__ void __launch_bounds__(32 * kWeighWarps, D == 256 ? 2 : 4)
   __shared__ int s_ptr[kMaxDraft];
   __shared__ float s_lse[RC];  // lse * log2(e); +inf for a row that counts nothing
   __shared__ int s_tok[RC];
-  __shared__ int64_t s_scan[THREADS / 32], s_found[2];
+  __shared__ int64_t s_scan[2 * (THREADS / 32)], s_found[2];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int lr = lane >> 2, lc = lane & 3;
   int64_t cur, end, seq_first;
-  int seq;
+  int seq, extra = 0;
   find_range<THREADS>(P.s, P.g, P.H, kAllRows, kTile, nullptr, blockIdx.x, gridDim.x, s_scan,
-                      s_found, cur, end, seq, seq_first);
+                      s_found, cur, end, seq, seq_first, extra);
   if (cur >= end) return;
   int masked_seq = -1;
   SeqView sv = seq_view(P.s, seq, false);

@@ -34,7 +34,7 @@ __global__ void __launch_bounds__(weigh_tc_threads<MX>(), 1)
   __shared__ __align__(16) float s_lse[kWeighRows];  // lse * log2(e); +inf behind the rows
   __shared__ int s_row[kWeighRows];                  // rows that count
   __shared__ int s_warp[8];
-  __shared__ int64_t s_scan[THREADS / 32], s_found[2];
+  __shared__ int64_t s_scan[2 * (THREADS / 32)], s_found[2];
   __shared__ uint64_t s_full[8], s_empty[8], s_score[2], s_free[2], s_query, s_drain;
   __shared__ uint64_t s_raw_full[F::kRaw], s_raw_empty[F::kRaw];
   __shared__ uint32_t s_tmem;
@@ -66,9 +66,9 @@ __global__ void __launch_bounds__(weigh_tc_threads<MX>(), 1)
   if (warp == 0) tmem_alloc(&s_tmem, 512);
   tc_fence_before();
   int64_t cur, end, seq_first;
-  int seq;
+  int seq, extra = 0;
   find_range<THREADS>(P.s, P.g, P.H, kAllRows, TN, nullptr, blockIdx.x, gridDim.x, s_scan, s_found,
-                      cur, end, seq, seq_first);  // barriers inside
+                      cur, end, seq, seq_first, extra);  // barriers inside
   tc_fence_after();
   const uint32_t tmem = s_tmem;
 
