@@ -255,3 +255,22 @@ def test_captured_serving_step(mx):
         for t, s in zip(kv, cache):
             assert torch.equal(t.view(torch.uint8), s.view(torch.uint8))
     assert int(d["err"]) == 0
+
+
+@pytest.mark.parametrize("mx", [False, True])
+def test_two_calls_at_once(mx):
+    """Different calls overlapping on two streams, each with a workspace of its own."""
+    scenes = [Scene([3000, 50], [20, 3], 2, 128, 4, 64, mx, "padded", seed=400),
+              Scene([900, 1700, 4], [1, 2, 1], 2, 128, 4, 16, mx, "chain", seed=401)]
+    devs = [sc.device() for sc in scenes]
+    want = [sc.attend(d) for sc, d in zip(scenes, devs)]
+    ws = [b.tree_attention_workspace(d["q"], d["kv"][0], sc.S, sc.max_draft) for sc, d in zip(scenes, devs)]
+    streams = [torch.cuda.Stream() for _ in scenes]
+    outs = [[torch.zeros_like(w) for _ in range(8)] for w in want]
+    torch.cuda.synchronize()
+    for r in range(8):
+        for sc, d, w, s, o in zip(scenes, devs, ws, streams, outs):
+            sc.attend(d, out=o[r], workspace=w, stream=s)
+    torch.cuda.synchronize()
+    for w, o in zip(want, outs):
+        assert all(torch.equal(x, w) for x in o)
