@@ -144,11 +144,13 @@ __global__ void __launch_bounds__(weigh_tc_threads<MX>(), 1)
           const int c = tid % (D / 8);
           const uint16_t* qp =
               P.q + sv.a * P.q_tok + static_cast<int64_t>(h) * P.g * P.q_head + c * 8;
-          for (int r0 = tid / (D / 8); r0 < n; r0 += 8 * kStep) {
+          const int fill = max(16, (n + 15) & ~15);  // rows of the product
+          for (int r0 = tid / (D / 8); r0 < fill; r0 += 8 * kStep) {
             uint4 v[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
               const int rr = r0 + i * kStep;
+              v[i] = make_uint4(0, 0, 0, 0);
               if (rr < n) {
                 const int row = s_row[rr], tk = row / P.g;
                 v[i] = ld_ro(qp + tk * P.q_tok + (row - tk * P.g) * P.q_head);
@@ -157,7 +159,7 @@ __global__ void __launch_bounds__(weigh_tc_threads<MX>(), 1)
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
               const int rr = r0 + i * kStep;
-              if (rr < n)
+              if (rr < fill)
                 sts16(smem + (c >> 3) * q_block + rr * 128 + (((c & 7) ^ (rr & 7)) << 4),
                       tc_order<MX>(v[i]));
             }
