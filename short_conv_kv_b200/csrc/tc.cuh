@@ -233,7 +233,7 @@ __device__ __noinline__ bool e4m3x16_slow(uint4 w, uint32_t sb, bool clean, uint
 // MXFP8: three warps bring the codes and scale bytes to a raw ring of kRaw
 // units, eight warps write them to the unit as bf16 (exact).  (With one kind of
 // warp for both, the addresses and copies stood between a unit's decoding and the
-// next one's: 3,200 cycles a unit instead of 1,700.)
+// next one's: 3,200 cycles a unit, so 2,030.)
 //
 // One call site brings all units: several copies of this code, with the
 // softmax's, fall out of the instruction cache.
