@@ -46,7 +46,7 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const Evic
   const cg::cluster_group cluster = cg::this_cluster();
   const int ctas = static_cast<int>(cluster.num_blocks());
   const int rank = static_cast<int>(cluster.block_rank());
-  extern __shared__ uint32_t s_keys[];
+  extern __shared__ __align__(16) uint32_t s_keys[];  // room + 128 words
   __shared__ uint32_t s_hist[2][256], s_all[256];
   __shared__ uint32_t s_prefix;
   __shared__ int s_need;
@@ -93,14 +93,27 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const Evic
       const int shift = 24 - 8 * step;
       uint32_t* hist = s_hist[step & 1];
       const uint32_t above = step == 0 ? 0u : 0xffffffffu << (shift + 8);
-      for (int p = c0 + warp * 32; p < c1; p += kSelectThreads) {
-        const bool in = p + lane < c1;
-        const uint32_t key = in ? key_at(p + lane) : 0u;
+      // one key: equal bins (weights are often equal) are added once a warp
+      auto tally = [&](uint32_t key, bool in) {
         const bool mine = in && (key & above) == prefix;
+        if (!__any_sync(kFullMask, mine)) return;
         const uint32_t bin = mine ? (key >> shift) & 255u : 256u;
-        // equal bins (weights are often equal) are added once a warp
         const unsigned same = __match_any_sync(kFullMask, bin);
         if (mine && lane == __ffs(same) - 1) atomicAdd(&hist[bin], __popc(same));
+      };
+      if (held) {  // four keys a lane; the slice begins on a multiple of 1024
+        const int n = c1 - a;
+        for (int q = (c0 - a) / 128 * 128 + warp * 128; q < n; q += 4 * kSelectThreads) {
+          const int x = q + 4 * lane;
+          const uint4 k = *reinterpret_cast<const uint4*>(s_keys + x);
+          tally(k.x, x >= c0 - a && x < n);
+          tally(k.y, x + 1 >= c0 - a && x + 1 < n);
+          tally(k.z, x + 2 >= c0 - a && x + 2 < n);
+          tally(k.w, x + 3 >= c0 - a && x + 3 < n);
+        }
+      } else {
+        for (int p = c0 + warp * 32; p < c1; p += kSelectThreads)
+          tally(p + lane < c1 ? weight_key(w[p + lane]) : 0u, p + lane < c1);
       }
       cluster.sync();
       if (tid < 256) {
@@ -159,12 +172,15 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const Evic
     }
   };
   int2 count = make_int2(0, 0);
+#pragma unroll 4
   for (int p = p0; p < p1; p += 32) {
     bool more, same;
     classify(p + lane, more, same);
-    count.x += __popc(__ballot_sync(kFullMask, more));
-    count.y += __popc(__ballot_sync(kFullMask, same));
+    count.x += more;
+    count.y += same;
   }
+  count.x = __reduce_add_sync(kFullMask, count.x);
+  count.y = __reduce_add_sync(kFullMask, count.y);
   if (lane == 0) s_count[warp] = count;
   __syncthreads();
   int2 before = make_int2(0, 0);

@@ -438,10 +438,10 @@ int evict_impl(const float* weights, int64_t positions, int64_t w_seq, int64_t w
     const int64_t slice = (A.q.capacity / c + 1025) / 1024 * 1024 + 1024;
     int room = static_cast<int>(std::min<int64_t>(slice, 48 * 1024));
     const void* fn = sconv::evict_select_fn();
-    if (!smem_attr_set(fn, 4 * static_cast<size_t>(room))) return SCONV_KV_ERR_CUDA;
+    const size_t smem = 4 * (static_cast<size_t>(room) + 128);  // read four keys at a time
+    if (!smem_attr_set(fn, smem)) return SCONV_KV_ERR_CUDA;
     void* args[] = {&A, &room};
-    rc = launch_clusters(fn, dim3(H * c, seqs->num_seqs), c, sconv::kSelectThreads,
-                         4 * static_cast<size_t>(room), args, stream);
+    rc = launch_clusters(fn, dim3(H * c, seqs->num_seqs), c, sconv::kSelectThreads, smem, args, stream);
     if (rc != SCONV_KV_OK) return rc;
   }
   const int c = spread(2 * units, 1);
