@@ -4,7 +4,8 @@ Argument marshalling only: every function takes torch tensors, passes their
 device pointers, sizes and the current CUDA stream to the C ABI declared in
 ``include/sconv_kv.h``, and raises on a non-zero status.  All of the step's
 work runs in the library's CUDA kernels; there is no CPU fallback, and if the
-library is missing the import fails loudly.
+library is missing the import fails loudly.  The drafted-tree and eviction calls
+marshal in compiled code (``_tree.so``).
 """
 import ctypes
 import os
