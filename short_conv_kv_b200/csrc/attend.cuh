@@ -23,10 +23,11 @@
 // independent, so the output's error stays below its own bf16 rounding), and the
 // output.
 //
-// Masked keys: their score is replaced by -inf before the maximum, and a V row
-// that nobody or not everybody may see is cleaned of NaN and infinities before the
+// Masked keys: their score is replaced by -inf before the maximum, and a drafted V row
+// (that nobody or not everybody may see) is cleaned of NaN and infinities before the
 // product (0 * inf would reach rows that do not see it); rows that do see
-// such a value get it back afterwards (restore_nonfinite).
+// such a value get it back afterwards (restore_nonfinite).  The context's rows,
+// which every used token sees, stay as they are.
 #pragma once
 #include "paged.cuh"
 
@@ -548,7 +549,9 @@ __global__ void __launch_bounds__(32 * kRowsWarps, D == 256 ? 2 : NT == 1 ? 4 : 
       if (tail) {
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
-          const bool vis = (seen >> (2 * lc + (t & 1) + (t >> 1) * 8)) & 1u;
+          const int key = 2 * lc + (t & 1) + (t >> 1) * 8;
+          if (base + key < sv.ctx) continue;  // the context, which all rows see: as it is
+          const bool vis = (seen >> key) & 1u;
 #pragma unroll
           for (int k = 0; k < VV; ++k) {
             if (vis)
