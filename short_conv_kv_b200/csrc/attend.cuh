@@ -256,28 +256,37 @@ __device__ __forceinline__ int q_dim(int t, int c) {
   return MX ? (t >> 1) * 64 + c * 16 + (t & 1) * 8 : t * 32 + c * 8;
 }
 
-template <bool MX>
+// Eight bf16 values, NaN and infinities as 0.
 __device__ __forceinline__ uint4 clean16(uint4 x, bool& found) {
   uint32_t* w = reinterpret_cast<uint32_t*>(&x);
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
-    if constexpr (MX) {
-#pragma unroll
-      for (int b = 0; b < 32; b += 8)
-        if (((w[e] >> b) & 0x7fu) == 0x7fu) {
-          w[e] &= ~(0xffu << b);
-          found = true;
-        }
-    } else {
-      if ((w[e] & 0x7f80u) == 0x7f80u) {
-        w[e] &= 0xffff0000u;
-        found = true;
-      }
-      if ((w[e] & 0x7f800000u) == 0x7f800000u) {
-        w[e] &= 0x0000ffffu;
-        found = true;
-      }
+    if ((w[e] & 0x7f80u) == 0x7f80u) {
+      w[e] &= 0xffff0000u;
+      found = true;
     }
+    if ((w[e] & 0x7f800000u) == 0x7f800000u) {
+      w[e] &= 0x0000ffffu;
+      found = true;
+    }
+  }
+  return x;
+}
+
+// Sixteen E4M3 codes of scale byte `s`, as 0 where they decode to NaN or an infinity.  A code with
+// exponent field E stands for a value of at least 2^(E - 7) (E > 0), times 2^(s - 127): from
+// E + s = 262 on that is 2^128, which no float holds; code 0x7f and scale 255 are NaN.
+__device__ __forceinline__ uint4 clean_codes(uint4 x, uint32_t s, bool& found) {
+  const uint32_t limit = s == 255u ? 0u : min(127u, (262u - s) * 8u);  // the first such code
+  uint32_t* w = reinterpret_cast<uint32_t*>(&x);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+#pragma unroll
+    for (int b = 0; b < 32; b += 8)
+      if (((w[e] >> b) & 0x7fu) >= limit) {
+        w[e] &= ~(0xffu << b);
+        found = true;
+      }
   }
   return x;
 }
@@ -554,16 +563,14 @@ __global__ void __launch_bounds__(32 * kRowsWarps, D == 256 ? 2 : NT == 1 ? 4 : 
           const bool vis = (seen >> key) & 1u;
 #pragma unroll
           for (int k = 0; k < VV; ++k) {
-            if (vis)
-              vreg[t][k] = clean16<MX>(vreg[t][k], found);
-            else
+            if (!vis)
               vreg[t][k] = make_uint4(0, 0, 0, 0);
+            else if constexpr (MX)
+              vreg[t][k] = clean_codes(vreg[t][k], vsc[t][k], found);
+            else
+              vreg[t][k] = clean16(vreg[t][k], found);
             if constexpr (MX)
-              if (!vis || vsc[t][k] == 255u) {
-                found |= vis;
-                vsc[t][k] = 0;
-                vreg[t][k] = make_uint4(0, 0, 0, 0);
-              }
+              if (!vis || vsc[t][k] == 255u) vsc[t][k] = 0;
           }
         }
       }

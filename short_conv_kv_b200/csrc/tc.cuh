@@ -212,8 +212,8 @@ __device__ __noinline__ bool e4m3x16_slow(uint4 w, uint32_t sb, bool clean, uint
   e4m3x4_bf16(w.w, sc, b.z, b.w);
   bool bad = false;
   if (clean) {
-    a = clean16<false>(a, bad);
-    b = clean16<false>(b, bad);
+    a = clean16(a, bad);
+    b = clean16(b, bad);
   }
   out[0] = tc_order<true>(a);
   out[1] = tc_order<true>(b);
@@ -317,7 +317,7 @@ struct FeedBf16 : FeedShape<D, KEYS, false> {
 #pragma unroll 1
         for (int b = 0; b < S::kBlocks; ++b) {
           bool bad = false;
-          const uint4 v = clean16<false>(lds16(place(j, b)), bad);
+          const uint4 v = clean16(lds16(place(j, b)), bad);
           if (bad) {
             sts16(place(j, b), v);
             R.abort[1] = 1;
