@@ -7,6 +7,7 @@ work runs in the library's CUDA kernels; there is no CPU fallback, and if the
 library is missing the import fails loudly.  The drafted-tree and eviction calls
 marshal in compiled code (``_tree.so``).
 """
+import contextlib
 import ctypes
 import os
 
@@ -685,20 +686,26 @@ def tree_attention_workspace(q, k_cache, num_seqs, max_draft):
 
 def _tree_attention(name, q, cu_draft, parents, context_lens, block_table, kc, ks, vc, vs, scale,
                     max_draft, out, lse, workspace, err_flag, stream):
-    if out is None:
-        out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
-    while True:
-        rc = _tree.tree_attention(q, cu_draft, parents, context_lens, block_table, kc, ks, vc, vs, scale,
-                                  max_draft, out, lse, workspace, err_flag, _on(stream))
-        if rc == 0:
-            return out
-        if rc < 0:
-            raise SconvKVError(rc, name)
-        workspace = tree_attention_workspace(q, kc, block_table.shape[0], max_draft)
-        if stream is not None:  # it is freed on return, and may be in use there
-            other = stream if isinstance(stream, torch.cuda.Stream) else \
-                torch.cuda.ExternalStream(_stream(stream), device=q.device)
-            workspace.record_stream(other)
+    if stream is None or not q.is_cuda or (out is not None and workspace is not None):
+        owner = contextlib.nullcontext()
+    else:
+        # What is allocated here has to be `stream`'s: a block of the current stream's pool may
+        # still be in use by kernels that nothing orders before this call.
+        if not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(int(stream), device=q.device) if int(stream) else \
+                torch.cuda.default_stream(q.device)
+        owner = torch.cuda.stream(stream)
+    with owner:
+        if out is None:
+            out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+        while True:
+            rc = _tree.tree_attention(q, cu_draft, parents, context_lens, block_table, kc, ks, vc, vs, scale,
+                                      max_draft, out, lse, workspace, err_flag, _on(stream))
+            if rc == 0:
+                return out
+            if rc < 0:
+                raise SconvKVError(rc, name)
+            workspace = tree_attention_workspace(q, kc, block_table.shape[0], max_draft)
 
 
 def tree_attention(q, cu_draft, parents, context_lens, block_table, k_cache, v_cache, scale,
@@ -709,8 +716,10 @@ def tree_attention(q, cu_draft, parents, context_lens, block_table, k_cache, v_c
     context_lens[i] + j.  max_draft: a host-side bound on the drafted tokens
     of a sequence.  Writes and returns out (bf16, q's shape) and fills lse
     (fp32 [T, Hq], natural logarithm) if given.  A chain of one token is the
-    plain decode.  Pass a workspace (tree_attention_workspace) to allocate
-    nothing, and under graph capture."""
+    plain decode.  Pass out and a workspace (tree_attention_workspace) to
+    allocate nothing, and under graph capture; what is not given is allocated
+    on `stream`, and an allocated out holds anything in the rows that no (good)
+    sequence has."""
     return _tree_attention("sconv_kv_tree_attention", q, cu_draft, parents, context_lens, block_table,
                            k_cache, None, v_cache, None, scale, max_draft, out, lse, workspace, err_flag,
                            stream)

@@ -68,3 +68,45 @@ def test_overflowing_scales_reach_nobody_else(scale, codes, n, D):
     rest = torch.ones(D, dtype=torch.bool)
     rest[32:64] = False
     assert torch.equal(got[n - 1, 4:][:, rest], clean[n - 1, 4:][:, rest])
+
+
+# --------------------------------------------- tensors allocated within a call
+
+def _segment_stream(t):
+    """The stream whose pool of the caching allocator holds t."""
+    for s in torch.cuda.memory_snapshot():
+        if s["address"] <= t.data_ptr() < s["address"] + s["total_size"]:
+            return s["stream"]
+    raise AssertionError("not the caching allocator's")
+
+
+@pytest.mark.parametrize("given", ["neither", "out", "workspace"])
+@pytest.mark.parametrize("handle", [False, True])
+@pytest.mark.parametrize("mx", [False, True])
+def test_allocations_belong_to_the_calls_stream(mx, handle, given, monkeypatch):
+    """What a call on another stream allocates for itself comes from that stream's memory: a block of the
+    current stream may still be in use by kernels that nothing orders before the call."""
+    sc = Scene([300, 20], [3, 9], 2, 64, 4, 16, mx, seed=530)
+    d = sc.device()
+    want = sc.attend(d)
+    made = []
+    make = b.tree_attention_workspace
+
+    def keep(*a):
+        made.append(make(*a))
+        return made[-1]
+    monkeypatch.setattr(b, "tree_attention_workspace", keep)
+    for stream in (torch.cuda.Stream(), torch.cuda.default_stream()):
+        made.clear()
+        out = torch.empty_like(want) if given == "out" else None
+        ws = make(d["q"], d["kv"][0], sc.S, sc.max_draft) if given == "workspace" else None
+        torch.cuda.synchronize()
+        current = torch.cuda.current_stream()
+        got = sc.attend(d, out=out, workspace=ws, stream=stream.cuda_stream if handle else stream)
+        assert torch.cuda.current_stream() == current
+        torch.cuda.synchronize()
+        assert torch.equal(got, want)
+        if given != "out":
+            assert _segment_stream(got) == stream.cuda_stream
+        if given != "workspace":
+            assert [_segment_stream(w) for w in made] == [stream.cuda_stream]
