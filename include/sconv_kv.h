@@ -619,7 +619,8 @@ SCONV_KV_API int sconv_kv_attention_weights_mxfp8(
  * state_positions (device int64 [num_seqs], or NULL) selects the ring state as in
  * sconv_kv_options_t: tokens seen before the path.  A bad leaf accepts
  * nothing (new_lens = ctx) and is flagged; a bad state index or negative
- * position leaves the state and is flagged.
+ * position leaves the state and is flagged.  With num_tokens == 0, new_lens is
+ * written all the same, and k, v and parents may be NULL.
  */
 SCONV_KV_API int sconv_kv_tree_accept(
     const void* k, const void* v, int64_t row_stride,

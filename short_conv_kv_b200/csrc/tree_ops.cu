@@ -77,7 +77,9 @@ int check_paged(const sconv_kv_paged_t* seqs, const sconv_kv_cache_layout_t* lay
   if (drafted && (seqs->max_draft < 1 || seqs->max_draft > SCONV_KV_MAX_DRAFT))
     return SCONV_KV_ERR_SHAPE;
   if (!seqs->context_lens || !seqs->block_table) return SCONV_KV_ERR_NULL;
-  if (drafted && (!seqs->cu_draft || !seqs->parents)) return SCONV_KV_ERR_NULL;
+  // (an empty tensor may have a NULL pointer)
+  if (drafted && (!seqs->cu_draft || (!seqs->parents && seqs->num_tokens > 0)))
+    return SCONV_KV_ERR_NULL;
   memset(Q, 0, sizeof *Q);
   if (drafted) {
     Q->cu = seqs->cu_draft;

@@ -110,3 +110,37 @@ def test_allocations_belong_to_the_calls_stream(mx, handle, given, monkeypatch):
             assert _segment_stream(got) == stream.cuda_stream
         if given != "workspace":
             assert [_segment_stream(w) for w in made] == [stream.cuda_stream]
+
+
+# ------------------------------------------------ batches with nothing drafted
+
+@pytest.mark.parametrize("W", [1, 4])
+@pytest.mark.parametrize("mx", [False, True])
+def test_batch_without_drafted_tokens(mx, W):
+    """T = 0: the lengths are written all the same, and nothing else changes."""
+    sc = Scene([30, 0, 17], [0, 0, 0], 2, 64, 4, 16, mx, seed=540)
+    d = sc.device()
+    before = [t.clone() for t in d["kv"]]
+    raw = torch.empty(0, 128, dtype=torch.bfloat16, device="cuda")
+    state = torch.randn(3, W - 1, 256, device="cuda").to(torch.bfloat16)
+    state0 = state.clone()
+    w = torch.rand(3, 2, 40, device="cuda")
+    w0 = w.clone()
+    new = torch.full((3,), -7, dtype=torch.int32, device="cuda")
+    leaves = torch.full((3,), -1, dtype=torch.int32, device="cuda")
+    fn = b.tree_accept_mxfp8 if mx else b.tree_accept
+    fn(raw, raw, d["cu"], d["parents"], leaves, d["lens"], d["table"], W, state if W > 1 else None, *d["kv"], new,
+       weights=w, err_flag=d["err"])
+    assert new.tolist() == [30, 0, 17] and int(d["err"]) == 0
+    assert torch.equal(state, state0) and torch.equal(w, w0)
+    for t, t0 in zip(d["kv"], before):
+        assert torch.equal(t.contiguous().view(torch.uint8), t0.contiguous().view(torch.uint8))
+    leaves[1] = 0  # a leaf that is no token
+    fn(raw, raw, d["cu"], d["parents"], leaves, d["lens"], d["table"], W, state if W > 1 else None, *d["kv"], new,
+       weights=w, err_flag=d["err"])
+    assert new.tolist() == [30, 0, 17] and int(d["err"]) == b.FLAG_TREE
+    assert sc.attend(d).shape == (0, 8, 64)
+    lse = torch.empty(0, 8, device="cuda")
+    (b.attention_weights_mxfp8 if mx else b.attention_weights)(
+        d["q"], lse, d["cu"], d["parents"], d["lens"], d["table"], *d["kv"][:2 if mx else 1], sc.scale, 1, w)
+    assert torch.equal(w, w0)
