@@ -139,7 +139,7 @@ CacheParts parts_of(const void* k, const void* v, const void* ks, const void* vs
 }
 
 int check_heads(int HQ, int H, int64_t tok, int64_t head, int D) {
-  if (H < 1 || HQ < H || HQ % H || HQ > (1 << 15)) return SCONV_KV_ERR_SHAPE;
+  if (H < 1 || HQ < H || HQ % H || HQ > sconv::kMaxQueryHeads) return SCONV_KV_ERR_SHAPE;
   if (head < D || tok < 1) return SCONV_KV_ERR_SHAPE;
   if (tok % 8 || head % 8) return SCONV_KV_ERR_ALIGN;
   return SCONV_KV_OK;
@@ -489,7 +489,8 @@ int sconv_kv_tree_attention_workspace(int num_seqs, int max_draft, int num_q_hea
                                       int num_kv_heads, int head_dim, int64_t* bytes) {
   if (!bytes) return SCONV_KV_ERR_NULL;
   if (num_seqs < 0 || max_draft < 1 || max_draft > SCONV_KV_MAX_DRAFT || num_kv_heads < 1 ||
-      num_q_heads < num_kv_heads || num_q_heads % num_kv_heads || num_q_heads > (1 << 15) ||
+      num_q_heads < num_kv_heads || num_q_heads % num_kv_heads ||
+      num_q_heads > sconv::kMaxQueryHeads ||
       !head_dim_ok(head_dim))
     return SCONV_KV_ERR_SHAPE;
   // enough for either store, and for calls with fewer drafted tokens, whose

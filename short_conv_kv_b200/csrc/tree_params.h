@@ -9,6 +9,9 @@ constexpr int kFlagTree = 16;
 constexpr int kFlagContext = 32;
 constexpr int kMaxDraft = 128;
 constexpr int kMaskWords = kMaxDraft / 32;
+constexpr int kMaxQueryHeads = 1 << 15;  // the host refuses more
+// Query rows of a K/V head at most: a unit of this many is one a (sequence, head).
+constexpr int kAllRows = kMaxDraft * kMaxQueryHeads;
 
 struct PagedSeqs {
   const int32_t* cu;       // [num_seqs + 1]; nullptr: no drafted tokens

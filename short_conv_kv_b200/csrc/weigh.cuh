@@ -25,7 +25,7 @@ __global__ void __launch_bounds__(32 * kWeighWarps, D == 256 ? 2 : 4)
     weigh_kernel(const WeighParams W) {
   using L = RowsLayout<D, MX>;
   constexpr int THREADS = 32 * kWeighWarps, KV = L::kKVec, RC = kWeighRowsQ<D>;
-  constexpr int kTile = 16 * kWeighWarps, kAllRows = 1 << 20;
+  constexpr int kTile = 16 * kWeighWarps;
   grid_dependency_wait();
   allow_dependent_launch();
   const AttendParams& P = W.a;

@@ -24,7 +24,7 @@ __host__ __device__ constexpr int weigh_tc_threads() {
 template <int D, bool MX>
 __global__ void __launch_bounds__(weigh_tc_threads<MX>(), 1)
     weigh_tc_kernel(const WeighParams W, int q_rows, int ring_units) {
-  constexpr int TN = 128, THREADS = weigh_tc_threads<MX>(), kSoft = 256, kAllRows = 1 << 20;
+  constexpr int TN = 128, THREADS = weigh_tc_threads<MX>(), kSoft = 256;
   using F = FeedShape<D, TN, MX>;
   grid_dependency_wait();
   allow_dependent_launch();
@@ -235,9 +235,9 @@ __global__ void __launch_bounds__(weigh_tc_threads<MX>(), 1)
         locate();
         const int64_t head = h * P.s.stride_head >> 5;
         const int low = P.c.words ? reinterpret_cast<uintptr_t>(P.c.ks + head) & 3 : 0;
-        const int passes = (all_rows + q_rows - 1) / q_rows;
+        const int64_t units_all = static_cast<int64_t>((all_rows + q_rows - 1) / q_rows) * tiles;
 #pragma unroll 1
-        for (int u = 0; u < passes * tiles; ++u)
+        for (int64_t u = 0; u < units_all; ++u)
           FeedMx<D, TN>::decode(R, Raw, w, lane, low, TN);
         cur += tiles;
       }
@@ -247,11 +247,11 @@ __global__ void __launch_bounds__(weigh_tc_threads<MX>(), 1)
         const uint8_t* kb = P.c.k + h * P.s.stride_head * 2;
         const int32_t* table = P.s.table + seq * P.s.table_stride;
         const int key0 = t0 * TN + w * F::kKeysWarp + lane % F::kKeysWarp;
-        const int units_all = (all_rows + q_rows - 1) / q_rows * tiles;
+        const int64_t units_all = static_cast<int64_t>((all_rows + q_rows - 1) / q_rows) * tiles;
         int page = __ldg(table + page_index(P.s, min(key0, total - 1)));
         int t = 0;
 #pragma unroll 1
-        for (int u = 0; u < units_all; ++u) {
+        for (int64_t u = 0; u < units_all; ++u) {
           const uint32_t off = paged_off8(P.s, page, key0 + t * TN, total);
           t = t + 1 == tiles ? 0 : t + 1;
           page = __ldg(table + page_index(P.s, min(key0 + t * TN, total - 1)));
@@ -319,7 +319,7 @@ __global__ void __launch_bounds__(weigh_tc_threads<MX>(), 1)
       const int64_t head = h * P.s.stride_head;
       const int32_t* table = P.s.table + seq * P.s.table_stride;
       const int key0 = t0 * TN + w * 8 + (lane >> 2);
-      const int units_all = (all_rows + q_rows - 1) / q_rows * tiles;
+      const int64_t units_all = static_cast<int64_t>((all_rows + q_rows - 1) / q_rows) * tiles;
       int page[M::kMine];
       auto pages = [&](int t) {
 #pragma unroll
@@ -329,7 +329,7 @@ __global__ void __launch_bounds__(weigh_tc_threads<MX>(), 1)
       pages(0);
       int t = 0;
 #pragma unroll 1
-      for (int u = 0; u < units_all; ++u) {
+      for (int64_t u = 0; u < units_all; ++u) {
         uint32_t off[M::kMine];
 #pragma unroll
         for (int i = 0; i < M::kMine; ++i) {

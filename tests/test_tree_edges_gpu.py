@@ -1,9 +1,10 @@
 """The drafted-tree operators at the edges of what their documentation allows."""
+import numpy as np
 import pytest
 import torch
 
 from short_conv_kv_b200 import binding as b
-from tests.tree_util import Scene
+from tests.tree_util import Scene, logit_error
 
 pytestmark = pytest.mark.gpu
 
@@ -144,3 +145,44 @@ def test_batch_without_drafted_tokens(mx, W):
     (b.attention_weights_mxfp8 if mx else b.attention_weights)(
         d["q"], lse, d["cu"], d["parents"], d["lens"], d["table"], *d["kv"][:2 if mx else 1], sc.scale, 1, w)
     assert torch.equal(w, w0)
+
+
+# --------------------------------------------------- the largest head groups
+
+@pytest.mark.parametrize("mx", [False, True])
+@pytest.mark.parametrize("H, group, n, D", [(2, 16384, 65, 64), (2, 16384, 65, 256), (1, 32768, 128, 64)])
+def test_weights_of_a_million_query_rows(H, group, n, D, mx):
+    """More than 2^20 query rows a K/V head, up to the largest that is taken: every head's own rows are
+    weighed, and nothing else is written."""
+    sc = Scene([20], [n], H, D, 1, 16, mx, "chain", seed=550)
+    d = sc.device()
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    q = torch.randn(n, H * group, D, generator=gen, device="cuda").to(torch.bfloat16)
+    lse = 14 + torch.rand(n, H * group, generator=gen, device="cuda")
+    w0 = torch.rand(1, H + 2, 20 + n + 3, generator=gen, device="cuda")
+    w = w0.clone()
+    fn = b.attention_weights_mxfp8 if mx else b.attention_weights
+    fn(q, lse, d["cu"], d["parents"], d["lens"], d["table"], *d["kv"][:2 if mx else 1], sc.scale, n,
+       w[:, 1:-1, :-3], d["err"])
+    assert int(d["err"]) == 0
+    p = np.arange(20 + n)
+    k = torch.from_numpy(sc.values(0)[sc.table[0, p // 16], p % 16]).cuda()  # [20 + n, H, D]
+    add = torch.zeros(H, 20 + n, dtype=torch.float64, device="cuda")
+    size = 0.0
+    for j in range(n):
+        x = q[j].double().view(H, group, D)
+        s = torch.einsum("hgd,phd->hgp", x, k[:21 + j]) * sc.scale
+        add[:, :21 + j] += torch.exp(s - lse[j].double().view(H, group, 1)).sum(1)
+        size = max(size, float(torch.einsum("hgd,phd->hgp", x.abs(), k[:21 + j].abs()).max() * sc.scale))
+    want = w0.double()
+    want[0, 1:-1, :20] += add[:, :20]
+    want[0, 1:-1, 20:-3] = add[:, 20:]
+    # a term's exponent: the score's error, lse * log2(e)'s rounding and the subtraction's, ex2's 2^-22; sums
+    # of positive terms: at most 2^6 additions in a pass of 64 rows or more, then one a pass, 2^-24 each of what
+    # is there
+    e = logit_error(size, D) + 2.0 ** -22 * (2 + 15) + (2 ** 6 + n * group / 64) * 2.0 ** -24
+    err = (w.double() - want).abs()
+    assert (err[0, 1:-1, :-3] <= e * want[0, 1:-1, :-3]).all(), (err[0, 1:-1, :-3] / want[0, 1:-1, :-3]).max() / e
+    rest = torch.ones_like(w, dtype=torch.bool)
+    rest[0, 1:-1, :-3] = False
+    assert torch.equal(w[rest], w0[rest])
