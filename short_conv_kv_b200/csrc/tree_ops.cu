@@ -156,10 +156,11 @@ struct AttendPlan {
   int tile;
   int threads;
   size_t smem;
+  int mtiles;  // of a (sequence, K/V head)
   int parts;
 };
 
-int plan_attend(int max_draft, int HQ, int H, int D, bool mx, AttendPlan* A) {
+int plan_attend(int num_seqs, int max_draft, int HQ, int H, int D, bool mx, AttendPlan* A) {
   const int rows = max_draft * (HQ / H);
   if (rows <= (D == 256 ? 8 : 16)) {
     const int nt = rows <= 8 ? 1 : 2;
@@ -179,6 +180,8 @@ int plan_attend(int max_draft, int HQ, int H, int D, bool mx, AttendPlan* A) {
     A->smem = t.smem;
     A->fn = reinterpret_cast<const void*>(t.fn);
   }
+  A->mtiles = (rows + A->rows - 1) / A->rows;
+  if (static_cast<int64_t>(num_seqs) * A->mtiles > INT32_MAX) return SCONV_KV_ERR_SHAPE;  // the join's grid
   if (!smem_attr_set(A->fn, A->smem)) return SCONV_KV_ERR_CUDA;
   A->parts = sm_count() * (A->units ? 1 : resident_per_sm(A->fn, A->threads, A->smem, 2));
   return SCONV_KV_OK;
@@ -212,7 +215,7 @@ int attention_impl(const void* q, int64_t q_tok, int64_t q_head, int HQ, int H, 
   if (!aligned(q, 16) || !aligned(out, 16) || !aligned(workspace, 16) || !aligned(lse, 4))
     return SCONV_KV_ERR_ALIGN;
   AttendPlan A;
-  rc = plan_attend(seqs->max_draft, HQ, H, D, mx, &A);
+  rc = plan_attend(seqs->num_seqs, seqs->max_draft, HQ, H, D, mx, &A);
   if (rc != SCONV_KV_OK) return rc;
   if (workspace_bytes < workspace_need(seqs->num_seqs, D, A.parts, A.rows))
     return SCONV_KV_ERR_SCRATCH;
@@ -240,14 +243,12 @@ int attention_impl(const void* q, int64_t q_tok, int64_t q_head, int HQ, int H, 
     rc = launch(A.fn, dim3(A.parts), dim3(A.threads), args, A.smem, stream);
     if (rc != SCONV_KV_OK) return rc;
   }
-  int mtiles = (seqs->max_draft * P.g + A.rows - 1) / A.rows;
-  const int64_t x = static_cast<int64_t>(seqs->num_seqs) * mtiles;
-  if (x > INT32_MAX) return SCONV_KV_ERR_SHAPE;
   const int rows = std::min(A.rows, seqs->max_draft * P.g);
   int split = rows <= 16;
-  void* args[] = {&P, &A.rows, &A.tile, &mtiles, &split};
+  void* args[] = {&P, &A.rows, &A.tile, &A.mtiles, &split};
   return launch(reinterpret_cast<const void*>(sconv::pick_attend_join(D)),
-                dim3(static_cast<unsigned>(x), H, split ? rows : (rows + 3) / 4), dim3(128), args, 0, stream);
+                dim3(static_cast<unsigned>(seqs->num_seqs) * A.mtiles, H, split ? rows : (rows + 3) / 4),
+                dim3(128), args, 0, stream);
 }
 
 int weights_impl(const void* q, int64_t q_tok, int64_t q_head, int HQ, int H, int D, float scale,
@@ -499,7 +500,7 @@ int sconv_kv_tree_attention_workspace(int num_seqs, int max_draft, int num_q_hea
   for (int mx = 0; mx < 2; ++mx)
     for (int n = 1; n <= max_draft; ++n) {
       AttendPlan A;
-      const int rc = plan_attend(n, num_q_heads, num_kv_heads, head_dim, mx != 0, &A);
+      const int rc = plan_attend(num_seqs, n, num_q_heads, num_kv_heads, head_dim, mx != 0, &A);
       if (rc != SCONV_KV_OK) return rc;
       need = std::max(need, workspace_need(num_seqs, head_dim, A.parts, A.rows));
     }
