@@ -5,7 +5,7 @@ device pointers, sizes and the current CUDA stream to the C ABI declared in
 ``include/sconv_kv.h``, and raises on a non-zero status.  All of the step's
 work runs in the library's CUDA kernels; there is no CPU fallback, and if the
 library is missing the import fails loudly.  The drafted-tree and eviction calls
-marshal in compiled code (``_tree.so``).
+marshal in compiled code (``_tree.so``, loaded by the first of them).
 """
 import contextlib
 import ctypes
@@ -635,7 +635,17 @@ def _load_tree():
     return module
 
 
-_tree = _load_tree()
+class _FirstCall:
+    """Stands for the marshalling module until one of these calls needs it: the step's own calls do
+    without."""
+
+    def __getattr__(self, name):
+        global _tree
+        _tree = _load_tree()
+        return getattr(_tree, name)
+
+
+_tree = _FirstCall()
 
 
 def _on(stream):

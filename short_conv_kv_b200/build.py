@@ -14,6 +14,7 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
+HEADER = os.path.join(INCLUDE, "sconv_kv.h")
 LIB = os.path.join(PKG, "libsconvkv.so")
 TREE = os.path.join(PKG, "_tree.so")
 TREE_SOURCE = os.path.join(CSRC, "tree_bind.cpp")
@@ -33,11 +34,18 @@ def nvcc():
     return cand if os.path.exists(cand) else "nvcc"
 
 
-def needs_build(out=LIB):
+def _older(out, deps):
+    """Whether `out` is missing, or older than one of `deps`."""
     if not os.path.exists(out):
         return True
     t = os.path.getmtime(out)
-    return any(os.path.getmtime(d) > t for d in DEPS if os.path.exists(d))
+    return any(os.path.getmtime(d) > t for d in deps if os.path.exists(d))
+
+
+def needs_build(out=LIB):
+    """Whether build(out) has something to do: the library, and beside its usual place the
+    marshalling module."""
+    return _older(out, DEPS) or (out == LIB and _older(TREE, [TREE_SOURCE, HEADER]))
 
 
 def _compile(src, obj, extra):

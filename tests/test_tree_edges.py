@@ -1,5 +1,10 @@
 """The drafted-tree calls at the edges of their arguments (CPU only: none touches a GPU)."""
+import os
+import subprocess
+import sys
+
 from short_conv_kv_b200 import binding as b
+from short_conv_kv_b200 import build
 from tests import test_tree_abi as abi
 
 
@@ -21,3 +26,53 @@ def test_too_many_tiles_for_the_join_are_refused_before_any_launch():
     many = 2 ** 31 - 1
     assert abi.attention(seqs=dict(num_seqs=many, max_draft=128)) == b.ERR_SHAPE
     assert abi.attention(seqs=dict(num_seqs=many, max_draft=128), mx=True) == b.ERR_SHAPE
+
+
+WITHOUT_MODULE = """
+import sys
+import torch
+from short_conv_kv_b200 import build
+build.TREE = build.TREE + ".absent"
+from short_conv_kv_b200 import binding as b
+assert b.version() > 0 and b.cache_layout(4, 16, 2, 64).head_dim == 64
+assert "short_conv_kv_b200._tree" not in sys.modules
+for _ in range(2):
+    try:
+        b.evict(*[torch.zeros(1)] * 5, 0, 0, torch.zeros(1, 1, 1), torch.zeros(1))
+    except ImportError as e:
+        assert "not built" in str(e)
+    else:
+        raise AssertionError("no error")
+build.TREE = build.TREE[:-len(".absent")]
+try:
+    b.evict(*[torch.zeros(1)] * 5, 0, 0, torch.zeros(1, 1, 1), torch.zeros(1))
+except TypeError:
+    print("fine")
+"""
+
+
+def test_the_steps_own_calls_do_without_the_marshalling_module():
+    """Where _tree.so is missing, the binding loads; the first call that needs the module says so."""
+    got = subprocess.run([sys.executable, "-c", WITHOUT_MODULE], capture_output=True, text=True, cwd=build.ROOT)
+    assert got.returncode == 0 and got.stdout.strip() == "fine", got.stderr
+
+
+def test_a_missing_or_old_marshalling_module_needs_a_build(tmp_path, monkeypatch):
+    lib, tree, src = tmp_path / "lib.so", tmp_path / "_tree.so", tmp_path / "tree_bind.cpp"
+    for f in (lib, tree, src):
+        f.write_text("")
+    at = max(os.path.getmtime(d) for d in build.DEPS)
+    for f, age in ((src, 0), (lib, 10), (tree, 10)):
+        os.utime(f, (at + age, at + age))
+    for name, f in (("LIB", lib), ("TREE", tree), ("TREE_SOURCE", src)):
+        monkeypatch.setattr(build, name, str(f))
+    assert not build.needs_build(str(lib))
+    os.utime(src, (at + 20, at + 20))
+    assert build.needs_build(str(lib))
+    os.utime(src, (at, at))
+    tree.unlink()
+    assert build.needs_build(str(lib))
+    other = tmp_path / "other.so"  # a library elsewhere has no module beside it
+    other.write_text("")
+    os.utime(other, (at + 10, at + 10))
+    assert not build.needs_build(str(other))
