@@ -549,7 +549,7 @@ SCONV_KV_API int sconv_kv_tree_step_mxfp8(
  *
  *  q          bf16, head hq of token t at q + t*q_token_stride +
  *             hq*q_head_stride; strides multiples of 8, 16-byte aligned.
- *  out        bf16, likewise; must not alias q.
+ *  out        bf16, likewise; its rows must not overlap, nor alias q.
  *  lse        fp32 [num_tokens, num_q_heads] or NULL.
  *  workspace  device scratch of at least the bytes that
  *             sconv_kv_tree_attention_workspace names, 16-byte aligned, with
@@ -583,8 +583,8 @@ SCONV_KV_API int sconv_kv_tree_attention_mxfp8(
 /*
  * Accumulated attention weights, the score that sconv_kv_evict goes by.
  * weights is fp32, position p < positions of head h of sequence i at
- * weights + i*seq_stride + h*head_stride + p; a sequence with more tokens than
- * that is skipped and flagged (SCONV_KV_FLAG_CONTEXT; so too in
+ * weights + i*seq_stride + h*head_stride + p, in rows that do not overlap; a
+ * sequence with more tokens than that is skipped and flagged (SCONV_KV_FLAG_CONTEXT; so too in
  * sconv_kv_tree_accept and sconv_kv_evict).  With add = sum over the used drafted tokens that
  * see p, and the query heads of h, of exp(scale * q . k_p - lse),
  *     weights += add  for p < context_lens[i],

@@ -134,6 +134,23 @@ Cache caches(const Tensor& k, const Maybe& ks, const Maybe& v, const Maybe& vs, 
   return c;
 }
 
+// Whether two of the n1 x n2 rows of `len` elements at i * s1 + j * s2 share an element.
+bool rows_overlap(int64_t n1, int64_t s1, int64_t n2, int64_t s2, int64_t len) {
+  if (n1 <= 0 || n2 <= 0 || len <= 0) return false;
+  if (n2 == 1 || (n1 > 1 && s1 < s2)) {
+    std::swap(n1, n2);
+    std::swap(s1, s2);
+  }
+  // n2 = 1: a single row; else s2 is the smaller stride of those in use
+  if (n2 > 1 && s2 < len) return true;
+  for (int64_t i = 1; i < n1 && i * s1 < (n2 - 1) * s2 + len; ++i) {
+    // from the last of the n2 rows that begins at or before this one, and to the next of them
+    const int64_t off = i * s1 % s2;
+    if (off < len || (off > s2 - len && i * s1 / s2 + 1 < n2)) return true;
+  }
+  return false;
+}
+
 // bf16 [T, Hq, D] with unit dim stride.
 struct Heads {
   void* p;
@@ -188,7 +205,7 @@ Weights weight_rows(const Maybe& t, const char* name, int64_t S, int64_t H, int 
     bad_value(std::string(name) + " must be [" + std::to_string(S) + ", " + std::to_string(H) +
               ", positions] with unit position stride");
   w.positions = t->size(2);
-  if ((S > 1 && t->stride(0) < w.positions) || (H > 1 && t->stride(1) < w.positions))
+  if (rows_overlap(S, t->stride(0), H, t->stride(1), w.positions))
     bad_value(std::string(name) + "'s rows must not overlap");
   on_device(*t, name, dev);
   w.p = static_cast<float*>(t->data_ptr());
@@ -292,6 +309,7 @@ int tree_attention(const Tensor& q, const Tensor& cu, const Tensor& parents, con
   if (D != c.lay.head_dim) bad_value("q and the cache differ in head_dim");
   if (out.sizes() != q.sizes()) bad_value("out must have q's shape");
   const Heads ho = heads(out, "out", dev);
+  if (rows_overlap(T, ho.tok, HQ, ho.head, D)) bad_value("out's rows must not overlap");
   auto* l = dense<float>(lse, "lse", at::kFloat, {T, HQ}, dev);
   const Seqs seqs = paged(lens, table, dev, &cu, &parents, T, max_draft);
   int* e = flag(err, dev);

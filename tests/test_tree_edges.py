@@ -1,7 +1,11 @@
 """The drafted-tree calls at the edges of their arguments (CPU only: none touches a GPU)."""
 import os
+import random
 import subprocess
 import sys
+
+import pytest
+import torch
 
 from short_conv_kv_b200 import binding as b
 from short_conv_kv_b200 import build
@@ -76,3 +80,41 @@ def test_a_missing_or_old_marshalling_module_needs_a_build(tmp_path, monkeypatch
     other.write_text("")
     os.utime(other, (at + 10, at + 10))
     assert not build.needs_build(str(other))
+
+
+def _strided(sizes, strides, dtype):
+    """A view of those strides, which may overlap."""
+    room = 1 + sum(max(n - 1, 0) * s for n, s in zip(sizes, strides))
+    return torch.zeros(room, dtype=dtype).as_strided(sizes, strides)
+
+
+def _overlaps(n1, s1, n2, s2, length):
+    seen = [i * s1 + j * s2 + e for i in range(n1) for j in range(n2) for e in range(length)]
+    return len(set(seen)) < len(seen)
+
+
+def test_overlapping_rows_are_refused_and_others_not():
+    """Weights and outputs whose rows share elements in any way would be written by several warps at once.  CPU
+    tensors: a layout that is accepted meets the device check instead."""
+    rng = random.Random(3)
+    i32, bf = torch.int32, torch.bfloat16
+    counts = [0, 0]
+    for _ in range(3000):
+        S, H, n = rng.randint(1, 6), rng.randint(1, 6), rng.randint(0, 9)
+        st = (rng.randint(0, 40), rng.randint(0, 40))
+        w = _strided((S, H, n), (*st, 1), torch.float32)
+        bad = _overlaps(S, st[0], H, st[1], n)
+        counts[bad] += 1
+        with pytest.raises(ValueError, match="overlap" if bad else "CUDA device"):
+            b.attention_weights(torch.zeros(3, H, 64, dtype=bf), torch.zeros(3, H), torch.zeros(S + 1, dtype=i32),
+                                torch.zeros(3, dtype=i32), torch.zeros(S, dtype=i32), torch.zeros(S, 4, dtype=i32),
+                                torch.zeros(8, 16, H, 64, dtype=bf), 1.0, 2, w)
+    assert min(counts) > 500
+    q, cu, par = torch.zeros(3, 4, 64, dtype=bf), torch.zeros(3, dtype=i32), torch.zeros(3, dtype=i32)
+    kc, lens, table = torch.zeros(8, 16, 2, 64, dtype=bf), torch.zeros(2, dtype=i32), torch.zeros(2, 4, dtype=i32)
+    for st, bad in (((256, 64), 0), ((64, 192), 0), ((64, 200), 0), ((128, 64), 1), ((64, 64), 1), ((64, 128), 1),
+                    ((72, 8), 1), ((144, 72), 1), ((216, 72), 1), ((72, 216), 0), ((288, 72), 0), ((192, 128), 1),
+                    ((320, 128), 0), ((448, 128), 0), ((8, 256), 1)):
+        with pytest.raises(ValueError, match="overlap" if bad else "CUDA device"):
+            b.tree_attention(q, cu, par, lens, table, kc, kc, 1.0, 2, out=_strided((3, 4, 64), (*st, 1), bf),
+                             workspace=torch.zeros(8, dtype=torch.uint8))
