@@ -615,7 +615,8 @@ SCONV_KV_API int sconv_kv_attention_weights_mxfp8(
  * where weights is not NULL, the weight) of position ctx + a_r moves to
  * ctx + r, the conv_state takes the last W-1 rows of (state ++ the path's raw
  * k/v rows), and new_lens[i] = ctx + m.  k, v, row_stride: the raw rows given to
- * sconv_kv_tree_step.  new_lens must not alias context_lens.  W == 1: no state.
+ * sconv_kv_tree_step.  new_lens must not alias context_lens or leaves.  W == 1:
+ * no state.
  * state_positions (device int64 [num_seqs], or NULL) selects the ring state as in
  * sconv_kv_options_t: tokens seen before the path.  A bad leaf accepts
  * nothing (new_lens = ctx) and is flagged; a bad state index or negative

@@ -771,7 +771,7 @@ def tree_accept(k, v, cu_draft, parents, leaves, context_lens, block_table, W, c
     """Accept the path that ends at draft leaves[i] (int32 [S], local index; -1:
     none) of every sequence: its cache rows (and weights, if given) move to
     the positions behind the context, conv_state takes its raw rows, and
-    new_lens (int32 [S], not context_lens itself) gets the new lengths.  k,
+    new_lens (int32 [S], not context_lens or leaves) gets the new lengths.  k,
     v: the raw rows that tree_step was given."""
     rc = _tree.tree_accept(k, v, cu_draft, parents, leaves, context_lens, block_table, W, conv_state, k_cache,
                            None, v_cache, None, new_lens, weights, state_indices, state_positions, err_flag,

@@ -356,7 +356,8 @@ int accept_impl(const void* k, const void* v, int64_t row_stride, const sconv_kv
     return SCONV_KV_ERR_SHAPE;
   if (weights) A.q.capacity = std::min(A.q.capacity, positions);
   if (W > 1 && !state) return SCONV_KV_ERR_NULL;
-  if (new_lens == seqs->context_lens) return SCONV_KV_ERR_SHAPE;
+  // (the blocks of a sequence read both while the first of them writes)
+  if (new_lens == seqs->context_lens || new_lens == leaves) return SCONV_KV_ERR_SHAPE;
   if (row_stride % 8 || !aligned(k, 16) || !aligned(v, 16) || !aligned(state, 16) ||
       !aligned(weights, 4))
     return SCONV_KV_ERR_ALIGN;

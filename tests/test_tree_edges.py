@@ -118,3 +118,9 @@ def test_overlapping_rows_are_refused_and_others_not():
         with pytest.raises(ValueError, match="overlap" if bad else "CUDA device"):
             b.tree_attention(q, cu, par, lens, table, kc, kc, 1.0, 2, out=_strided((3, 4, 64), (*st, 1), bf),
                              workspace=torch.zeros(8, dtype=torch.uint8))
+
+
+def test_accept_refuses_lengths_written_over_the_leaves():
+    """A sequence's blocks read its leaf while the first of them writes its length."""
+    for mx in (False, True):
+        assert abi.accept(leaves=abi.A + 64, mx=mx) == b.ERR_SHAPE  # new_lens' address
