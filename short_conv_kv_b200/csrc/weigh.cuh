@@ -32,7 +32,7 @@ __global__ void __launch_bounds__(32 * kWeighWarps, D == 256 ? 2 : 4)
   extern __shared__ __align__(16) uint8_t smem[];  // Q
   __shared__ uint32_t s_anc[kMaxDraft][kMaskWords];
   __shared__ int s_ptr[kMaxDraft];
-  __shared__ float s_lse[RC];  // lse * log2(e); +inf for a row that counts nothing
+  __shared__ __align__(16) float s_lse[RC];  // lse * log2(e); +inf for a row that counts nothing
   __shared__ int s_tok[RC];
   __shared__ int64_t s_scan[2 * (THREADS / 32)], s_found[2];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
