@@ -186,3 +186,27 @@ def test_weights_of_a_million_query_rows(H, group, n, D, mx):
     rest = torch.ones_like(w, dtype=torch.bool)
     rest[0, 1:-1, :-3] = False
     assert torch.equal(w[rest], w0[rest])
+
+
+# --------------------------------- masked rows, where several CTAs share a unit
+
+@pytest.mark.parametrize("mx", [False, True])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("ctx, n", [(2000, 2), (2003, 2), (2000, 20), (1985, 50), (1900, 128)])
+def test_masked_nonfinite_rows_in_cut_units(ctx, n, D, mx):
+    """A drafted row with NaN in K and V, in a context that is cut into parts: its own token is NaN, its
+    siblings' bits and the padding's zeros are as they were."""
+    sc = Scene([ctx], [n], 1, D, 4, 16, mx, "star", seed=560)
+    d = sc.device()
+    if n > 8:
+        d["parents"][n - 3] = -2  # padding among them
+    clean = sc.attend(d).clone()
+    p = ctx + n - 2
+    pg, off = int(sc.table[0, p // 16]), p % 16
+    for t in d["kv"]:
+        t[pg, off] = 0xFF if t.dtype == torch.uint8 else float("nan")
+    got = sc.attend(d)
+    assert torch.isnan(got[n - 2]).all()
+    others = torch.arange(n, device="cuda") != n - 2
+    assert torch.equal(got[others], clean[others]) and torch.isfinite(got[others]).all()
+    assert int(d["err"]) == 0
