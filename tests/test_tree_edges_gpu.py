@@ -4,7 +4,7 @@ import pytest
 import torch
 
 from short_conv_kv_b200 import binding as b
-from tests.tree_util import Scene, logit_error
+from tests.tree_util import Scene, check_attention, logit_error
 
 pytestmark = pytest.mark.gpu
 
@@ -209,4 +209,159 @@ def test_masked_nonfinite_rows_in_cut_units(ctx, n, D, mx):
     assert torch.isnan(got[n - 2]).all()
     others = torch.arange(n, device="cuda") != n - 2
     assert torch.equal(got[others], clean[others]) and torch.isfinite(got[others]).all()
+    assert int(d["err"]) == 0
+
+
+# ------------------------------------------------- one step under other layouts
+
+def _five_calls(sc, d, seed):
+    """Step, attention, weights, acceptance and eviction on the scene's cache; everything they leave."""
+    H, D, W, T, S, g = sc.H, sc.D, 4, sc.T, sc.S, sc.group
+    C = H * D
+    fn = {n: getattr(b, n + ("_mxfp8" if sc.mx else ""))
+          for n in ("tree_step", "tree_attention", "attention_weights", "tree_accept", "evict")}
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    rnd = lambda *s: torch.randn(*s, generator=gen, device="cuda").to(torch.bfloat16)  # noqa: E731
+    raw, taps, state = rnd(2, T, C), rnd(2, W, C), rnd(S, W - 1, 2 * C)
+    gamma = torch.ones(D, device="cuda")
+    pos = np.concatenate([c + np.arange(n) for c, n in zip(sc.lens, sc.drafts)])
+    seq = np.repeat(np.arange(S), sc.drafts)
+    slots = torch.from_numpy(sc.table[seq, pos // sc.page].astype(np.int64) * sc.page + pos % sc.page).cuda()
+    at = (d["cu"], d["parents"])
+    fn["tree_step"](raw[0], raw[1], *at, taps[0], taps[1], gamma, gamma, 1e-6, state, slots, *d["kv"],
+                    err_flag=d["err"])
+    lse = torch.full((T, H * g), 7.0, device="cuda")
+    out = fn["tree_attention"](d["q"], *at, d["lens"], d["table"], *d["kv"], sc.scale, sc.max_draft, lse=lse,
+                               err_flag=d["err"])
+    w = torch.rand(S, H, sc.table.shape[1] * sc.page, generator=gen, device="cuda")
+    fn["attention_weights"](d["q"], lse, *at, d["lens"], d["table"], *d["kv"][:2 if sc.mx else 1], sc.scale,
+                            sc.max_draft, w, err_flag=d["err"])
+    leaves = torch.tensor([n - 1 for n in sc.drafts], dtype=torch.int32, device="cuda")
+    new, last = (torch.empty(S, dtype=torch.int32, device="cuda") for _ in range(2))
+    fn["tree_accept"](raw[0], raw[1], *at, leaves, d["lens"], d["table"], W, state, *d["kv"], new, weights=w,
+                      err_flag=d["err"])
+    kept, wo = torch.empty(S, H, 40, dtype=torch.int32, device="cuda"), torch.zeros_like(w)
+    fn["evict"](w, new, d["table"], *d["kv"], 2, 8, kept, last, wo, err_flag=d["err"])
+    torch.cuda.synchronize()
+    assert int(d["err"]) == 0
+    return [out, lse, w, state, new, kept, last, wo] + [t.contiguous() for t in d["kv"]]
+
+
+@pytest.mark.parametrize("layout, mx", [("heads first", False), ("heads first", True), ("far pages", False),
+                                        ("far pages", True), ("odd scales", True)])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("drafts", [[3, 1], [40, 9]])
+def test_layouts_give_the_same_bits(layout, drafts, D, mx):
+    """The five calls on the same rows in another layout: head-major pages, pages that lie past 2^32 elements,
+    scale bytes at odd addresses."""
+    # the tables' last pages are full to the last slot
+    sc = Scene([128 - drafts[0], 96 - drafts[1]], drafts, 2, D, 4, 16, mx, "chain", seed=570, width_extra=0)
+    d, e = sc.device(), sc.device()
+
+    def place(t, scales):
+        P, page, H, n = t.shape
+        if layout == "heads first":
+            return t.permute(0, 2, 1, 3).contiguous().permute(0, 2, 1, 3)
+        if layout == "far pages":  # the last page begins at 2^32 elements or behind (their scales: at 1/32 of that)
+            stride = (2 ** 32 // (P - 1) // 1024 + 1) * 1024 // (32 if scales else 1)
+            room = torch.empty((P - 1) * stride + page * H * n, dtype=t.dtype, device="cuda")
+            far = room.as_strided(t.shape, (stride, H * n, n, 1))
+            assert scales or (P - 1) * stride >= 2 ** 32
+            return far.copy_(t)
+        if not scales:
+            return t.contiguous()
+        room = torch.empty(t.numel() + 16, dtype=torch.uint8, device="cuda")
+        return room[odd.pop():][:t.numel()].view(t.shape).copy_(t)
+    odd = [3, 1]
+    e["kv"] = tuple(place(t, sc.mx and i % 2 == 1) for i, t in enumerate(d["kv"]))
+    if layout == "odd scales":
+        d["kv"] = tuple(t.contiguous() for t in d["kv"])
+    for x, y in zip(_five_calls(sc, d, 6), _five_calls(sc, e, 6)):
+        assert torch.equal(x.view(torch.uint8), y.view(torch.uint8))
+
+
+# ----------------------------------------------------------- counts at their ends
+
+@pytest.mark.parametrize("mx", [False, True])
+def test_no_sequence_at_all(mx):
+    """S = 0: every call returns, and nothing is written."""
+    sc = Scene([20], [2], 2, 64, 4, 16, mx, seed=580)
+    d = sc.device()
+    i32 = dict(dtype=torch.int32, device="cuda")
+    none, cu, table = torch.empty(0, **i32), torch.zeros(1, **i32), torch.empty(0, 4, **i32)
+    q, lse = torch.empty(0, 8, 64, dtype=torch.bfloat16, device="cuda"), torch.empty(0, 8, device="cuda")
+    raw = torch.empty(0, 128, dtype=torch.bfloat16, device="cuda")
+    w, kept = torch.empty(0, 2, 30, device="cuda"), torch.empty(0, 2, 9, **i32)
+    state = torch.empty(0, 3, 256, dtype=torch.bfloat16, device="cuda")
+    taps = torch.ones(4, 128, dtype=torch.bfloat16, device="cuda")
+    gamma = torch.ones(64, device="cuda")
+    before = [t.clone() for t in d["kv"]]
+    fn = {n: getattr(b, n + ("_mxfp8" if mx else ""))
+          for n in ("tree_step", "tree_attention", "attention_weights", "tree_accept", "evict")}
+    fn["tree_step"](raw, raw, cu, none, taps, taps, gamma, gamma, 1e-6, state,
+                    torch.empty(0, dtype=torch.int64, device="cuda"), *d["kv"])
+    assert fn["tree_attention"](q, cu, none, none, table, *d["kv"], 0.1, 3, lse=lse).shape == (0, 8, 64)
+    fn["attention_weights"](q, lse, cu, none, none, table, *d["kv"][:2 if mx else 1], 0.1, 3, w)
+    fn["tree_accept"](raw, raw, cu, none, none, none, table, 4, state, *d["kv"], torch.empty(0, **i32), weights=w)
+    fn["evict"](w, none, table, *d["kv"], 1, 2, kept, torch.empty(0, **i32))
+    torch.cuda.synchronize()
+    for t, t0 in zip(d["kv"], before):
+        assert torch.equal(t.contiguous().view(torch.uint8), t0.contiguous().view(torch.uint8))
+
+
+@pytest.mark.parametrize("max_draft", [1, 128])
+def test_seventy_thousand_sequences(max_draft):
+    """More sequences than a grid's smaller dimensions hold, some without a token: each one's result is its
+    own, with the few-row kernels and with the tensor cores'."""
+    S, H, D, g, page = 70001, 1, 64, 2, 4
+    gen = torch.Generator(device="cuda").manual_seed(8)
+    lens = torch.randint(0, 7, (S,), generator=gen, device="cuda").to(torch.int32)
+    n = (torch.rand(S, generator=gen, device="cuda") < 0.9).to(torch.int32)
+    cu = torch.cat([torch.zeros(1, dtype=torch.int32, device="cuda"), n.cumsum(0).to(torch.int32)])
+    T = int(cu[-1])
+    table = torch.randint(0, 500, (S, 2), generator=gen, device="cuda").to(torch.int32)  # shared pages
+    kc, vc = (torch.randn(500, page, H, D, generator=gen, device="cuda").to(torch.bfloat16) for _ in range(2))
+    q = torch.randn(T, g, D, generator=gen, device="cuda").to(torch.bfloat16)
+    par = torch.full((T,), -1, dtype=torch.int32, device="cuda")
+    lse, err = torch.empty(T, g, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = b.tree_attention(q, cu, par, lens, table, kc, vc, 0.125, max_draft, lse=lse, err_flag=err)
+    w = torch.ones(S, H, 8, device="cuda")
+    b.attention_weights(q, lse, cu, par, lens, table, kc, 0.125, max_draft, w, err)
+    assert int(err) == 0
+    seq = n.nonzero().flatten()
+    p = torch.arange(8, device="cuda")
+    page_of = table[seq].long().gather(1, (p // page).expand(T, 8))
+    k, v = (t[page_of, p % page, 0].double() for t in (kc, vc))  # [T, 8, D]
+    c = lens[seq].long()[:, None]
+    s = torch.einsum("tgd,tpd->tgp", q.double(), k) * 0.125
+    s.masked_fill_((p[None] > c)[:, None], -float("inf"))
+    prob = s.softmax(-1)
+    # as in tree_util.check_attention: roundings of the output and of the probabilities, then the fp32 parts
+    size = float(torch.einsum("tgd,tpd->tgp", q.double().abs(), k.abs()).max()) * 0.125
+    mag = torch.einsum("tgp,tpd->tgd", prob, v.abs())
+    want = torch.einsum("tgp,tpd->tgd", prob, v)
+    e = logit_error(size, D) + 2.0 ** -22 + 2.0 ** -11
+    assert ((out.double() - want).abs() <= 2.0 ** -8 * (want.abs() + mag) * 1.01 + 2 * e * mag).all()
+    ref = torch.logsumexp(s, -1)
+    assert ((lse.double() - ref).abs() <= logit_error(size, D) + 2.0 ** -20 + 2.0 ** -22 * ref.abs()).all()
+    add = torch.exp(s - lse.double()[..., None]).sum(1)
+    full = torch.ones(S, 8, dtype=torch.float64, device="cuda")
+    full[seq] = torch.where(p[None] < c, 1 + add, torch.where(p[None] == c, add, 1.0))
+    we = logit_error(size, D) + 2.0 ** -22 * (2 + float(lse.abs().max())) + 2.0 ** -20
+    assert ((w[:, 0].double() - full).abs() <= we * full).all()
+    # the same rows with every sequence's acceptance: lengths of all of them
+    new = torch.empty(S, dtype=torch.int32, device="cuda")
+    raw = torch.zeros(T, D, dtype=torch.bfloat16, device="cuda")
+    b.tree_accept(raw, raw, cu, par, n - 1, lens, table, 1, None, kc, vc, new, err_flag=err)
+    assert torch.equal(new, lens + n) and int(err) == 0
+
+
+@pytest.mark.parametrize("mx", [False, True])
+def test_a_bound_far_above_the_drafts(mx):
+    """max_draft is a bound: few tokens under a large one, on the kernels for many rows."""
+    sc = Scene([100, 700], [2, 1], 2, 128, 4, 64, mx, "chain", seed=590)
+    d = sc.device()
+    lse = torch.empty(sc.T, sc.HQ, device="cuda")
+    out = sc.attend(d, lse=lse, max_draft=128)
+    check_attention(out.double().cpu().numpy(), lse.double().cpu().numpy(), sc.oracle_attention(), 128)
     assert int(d["err"]) == 0
