@@ -63,6 +63,79 @@ __device__ __forceinline__ uint32_t seen32(const uint32_t* anc, int a0, bool use
   return __funnelshift_r(lo, hi, sh);
 }
 
+// Scores (times log2(e)) from 2^24 on lie 1 or more apart.  The softmax passes subtract a rounded maximum from
+// products that are not, which is then off by as much (from about 2^30 on the largest may come out as 0 or
+// infinite), and handling that in the passes costs 3 to 10 % of every call.  So a row whose maximum says that
+// it has met such scores is done again from the cache when its unit ends: rare, a thread a row, out of line, 0 to
+// 1.5 % for the calls that do not need it.  (All of 32 rows over 1,048,573 tokens: 218 ms, MXFP8 392.)
+__device__ __forceinline__ bool huge_score(float s) {
+  return fabsf(s) >= 0x1p24f && fabsf(s) < INFINITY;
+}
+// Keys key0 .. key1-1 of the row with query q and view `anc`: its maximum and sum, and its sums of V's columns
+// d0 .. d1-1 in acc[d0 ..].  Score products and maxima are both rounded.  The others' waits go by `steps`.
+template <int D, bool MX>
+__device__ __noinline__ float2 huge_row(const AttendParams& P, int seq, int ctx, int h, const uint32_t* anc,
+                                        int key0, int key1, const uint16_t* q, float* acc, int d0, int d1,
+                                        int* steps) {
+  const uint8_t* kb = P.c.k + h * P.s.stride_head * (MX ? 1 : 2);
+  const uint8_t* sb = MX ? P.c.ks + (h * P.s.stride_head >> 5) : nullptr;
+  const float scale = P.scale_log2;
+  float m = -INFINITY, l = 0.f, base = 0.f;
+#pragma unroll 1
+  for (int pass = 0; pass < 2; ++pass) {
+    uint32_t off = paged_off8(P.s, page_of(P.s, seq, key0), key0, key1);
+#pragma unroll 1
+    for (int p = key0; p < key1; ++p) {
+      const uint32_t here = off;
+      if ((p & 255) == 0) atomicAdd(steps, 1);
+      const int page = page_of(P.s, seq, min(p + 1, key1 - 1));  // the next row's
+      if (p < ctx || ((anc[(p - ctx) >> 5] >> ((p - ctx) & 31)) & 1u)) {
+        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll 2
+        for (int d = 0; d < D; d += 16) {
+          uint4 k[2];
+          if constexpr (MX) {
+            const uint4 w = *reinterpret_cast<const uint4*>(kb + static_cast<uint64_t>(here) * 8 + d);
+            const uint32_t sc = e8m0_bf16x2(sb[(here >> 2) + (d >> 5)]);
+            e4m3x4_bf16(w.x, sc, k[0].x, k[0].y);
+            e4m3x4_bf16(w.y, sc, k[0].z, k[0].w);
+            e4m3x4_bf16(w.z, sc, k[1].x, k[1].y);
+            e4m3x4_bf16(w.w, sc, k[1].z, k[1].w);
+          } else {
+            const uint4* from = reinterpret_cast<const uint4*>(kb + static_cast<uint64_t>(here) * 16 + d * 2);
+            k[0] = from[0];
+            k[1] = from[1];
+          }
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            float2 a[4], b[4];
+            unpack8(k[u], a);
+            unpack8(ld_ro(q + d + u * 8), b);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sum[u] = ffma2(a[e], b[e], sum[u]);
+          }
+        }
+        const float s = __fmul_rn((sum[0].x + sum[0].y) + (sum[1].x + sum[1].y), scale);
+        if (pass == 0) {
+          m = fmaxf(m, s);
+        } else {
+          const float w = ex2(__fsub_rn(s, base));
+          l += w;
+          const int64_t v = static_cast<int64_t>(here) * 8 + h * P.s.stride_head;
+          if (w != 0.f)  // seldom
+            for (int d = d0; d < d1; ++d) acc[d] = fmaf(w, cache_value<MX>(P.c.v, P.c.vs, v + d), acc[d]);
+        }
+      }
+      off = row_off8(P.s, page, min(p + 1, key1 - 1));
+    }
+    if (pass == 0) {
+      base = m == -INFINITY ? 0.f : m;
+      for (int d = d0; d < d1; ++d) acc[d] = 0.f;
+    }
+  }
+  return make_float2(m, l);
+}
+
 template <int D, bool MX>
 __global__ void __launch_bounds__(tc_threads<D, MX>(), 1)
     attend_tc_kernel(const AttendParams P, int rows_unit, int ring_units) {
@@ -81,7 +154,7 @@ __global__ void __launch_bounds__(tc_threads<D, MX>(), 1)
   __shared__ uint64_t s_full[8], s_empty[8], s_score[2], s_prob[2], s_out[2], s_query, s_drain;
   __shared__ uint64_t s_raw_full[F::kRaw], s_raw_empty[F::kRaw];
   __shared__ uint32_t s_tmem;
-  __shared__ int s_abort[2];  // a wait ran out; a V row was cleaned
+  __shared__ int s_abort[3];  // a wait ran out; a V row was cleaned; steps of huge_row()
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t smem = (smem_u32(smem_raw) + 1023u) & ~1023u;
   const uint32_t units = smem + (rows_unit > 128 || NS == 1 ? NS : 1) * kQTile;
@@ -105,7 +178,7 @@ __global__ void __launch_bounds__(tc_threads<D, MX>(), 1)
     mbar_init(&s_query, kSoft);
     mbar_init(&s_drain, 1);
     mbar_init_fence();
-    s_abort[0] = s_abort[1] = 0;
+    s_abort[0] = s_abort[1] = s_abort[2] = 0;
   }
   if (warp == 0) tmem_alloc(&s_tmem, 512);
   tc_fence_before();
@@ -164,7 +237,7 @@ __global__ void __launch_bounds__(tc_threads<D, MX>(), 1)
     int segment = 0, masked_seq = -1;
     bool ok = true;
     auto wait = [&](uint64_t* bar, uint32_t count) {  // until its phase `count` is complete
-      if (ok) ok = mbar_wait(bar, count & 1u, s_abort, kTcTimeoutNs);
+      if (ok) ok = tc_wait(bar, count & 1u, s_abort);
       ok = __all_sync(kFullMask, ok);
     };
     auto meet = [&] { asm volatile("bar.sync 1, %0;" ::"n"(kSoft) : "memory"); };
@@ -403,6 +476,17 @@ __global__ void __launch_bounds__(tc_threads<D, MX>(), 1)
               P.part_o[(slot * rows_unit + mine) * D + d] += v;
             }
           }
+        if (huge_score(mx) && used) {
+          float* acc = P.part_o + (slot * rows_unit + mine) * D;  // (its place, or free while the unit is whole)
+          const float2 r = huge_row<D, MX>(P, seq, sv.ctx, h, s_anc[tok], t0 * TN, min(total, (t0 + tiles) * TN),
+                                           P.q + (sv.a + tok) * P.q_tok + hq * P.q_head, acc, d0, d1, &s_abort[2]);
+          mx = r.x;
+          sum = r.y;
+          if (whole)
+            for (int d = d0; d < d1; ++d)
+              P.out[(sv.a + tok) * P.o_tok + hq * P.o_head + d] = static_cast<uint16_t>(
+                  pack_bf16x2(make_float2(sum == 0.f ? 0.f : acc[d] / sum, 0.f)));
+        }
         if (mine < rows && d0 == 0) {
           const float l = none ? 0.f : sum;
           if (!whole)
@@ -477,7 +561,7 @@ __global__ void __launch_bounds__(tc_threads<D, MX>(), 1)
     uint32_t phase = 0;
     bool ok = true;
     auto wait = [&](uint64_t* bar, uint32_t count) {
-      if (ok) ok = mbar_wait(bar, count & 1u, s_abort, kTcTimeoutNs);
+      if (ok) ok = tc_wait(bar, count & 1u, s_abort);
       ok = __all_sync(kFullMask, ok);
     };
     auto unit = [&](int at, uint32_t par) {  // until the unit is there

@@ -8,6 +8,30 @@ namespace sconv {
 
 constexpr uint64_t kTcTimeoutNs = 1000000000ull;
 
+// mbar_wait() for the roles of these kernels: abort[2] counts work that may hold a warpgroup up for longer than
+// the limit (rows that are done again, attend_tc.cuh); the limit runs from its last step, so a wait ends
+// when that work has.
+__device__ __forceinline__ bool tc_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  if (mbar_try_wait(bar, parity)) return true;
+  uint64_t t0 = global_ns();
+  int step = 0;
+  while (true) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (mbar_try_wait(bar, parity)) return true;
+    if (*abort) return false;
+    if (global_ns() - t0 > kTcTimeoutNs) {
+      const int now = abort[2];
+      if (now == step) {
+        *abort = 1;
+        return false;
+      }
+      step = now;
+      t0 = global_ns();
+    }
+  }
+}
+
 // ------------------------------------------------------------ tensor memory
 
 __device__ __forceinline__ void tmem_alloc(uint32_t* to, uint32_t cols) {  // one warp
@@ -242,14 +266,14 @@ struct FeedRing {
   uint32_t units;  // shared-memory address of the first unit
   uint64_t* full;
   uint64_t* empty;
-  volatile int* abort;  // [1]: a V row was cleaned
+  volatile int* abort;  // [1]: a V row was cleaned; [2]: as tc_wait() has it
   int count;            // units in the ring
 
   int slot = 0, phase = 0;  // the unit to fill next
   bool wrapped = false, ok = true;
 
   __device__ __forceinline__ void wait_empty() {
-    if (wrapped && ok && !mbar_wait(empty + slot, phase, abort, kTcTimeoutNs)) ok = false;
+    if (wrapped && ok && !tc_wait(empty + slot, phase, abort)) ok = false;
   }
   __device__ __forceinline__ void advance() {
     if (++slot == count) {
@@ -395,7 +419,7 @@ struct FeedMx : FeedShape<D, KEYS, true> {
   // The next raw unit to the next unit.
   static __device__ __forceinline__ void decode(FeedRing& R, FeedRing& Raw, int warp, int lane,
                                                 int low, int clean) {
-    if (Raw.ok && !mbar_wait(Raw.full + Raw.slot, Raw.phase, Raw.abort, kTcTimeoutNs)) Raw.ok = false;
+    if (Raw.ok && !tc_wait(Raw.full + Raw.slot, Raw.phase, Raw.abort)) Raw.ok = false;
     R.wait_empty();
     if (R.ok && Raw.ok) {
       const int chunk = (lane & 3) * 2, row0 = warp * S::kKeysWarp + (lane >> 2);

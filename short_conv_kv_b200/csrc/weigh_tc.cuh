@@ -39,7 +39,7 @@ __global__ void __launch_bounds__(weigh_tc_threads<MX>(), 1)
   __shared__ uint64_t s_full[8], s_empty[8], s_score[2], s_free[2], s_query, s_drain;
   __shared__ uint64_t s_raw_full[F::kRaw], s_raw_empty[F::kRaw];
   __shared__ uint32_t s_tmem;
-  __shared__ int s_abort[2], s_rows;
+  __shared__ int s_abort[3], s_rows;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t smem = (smem_u32(smem_raw) + 1023u) & ~1023u;
   const uint32_t q_block = q_rows * 128;
@@ -62,7 +62,7 @@ __global__ void __launch_bounds__(weigh_tc_threads<MX>(), 1)
     mbar_init(&s_query, kSoft);
     mbar_init(&s_drain, 1);
     mbar_init_fence();
-    s_abort[0] = s_abort[1] = 0;
+    s_abort[0] = s_abort[1] = s_abort[2] = 0;
   }
   if (warp == 0) tmem_alloc(&s_tmem, 512);
   tc_fence_before();
@@ -174,7 +174,7 @@ __global__ void __launch_bounds__(weigh_tc_threads<MX>(), 1)
           const bool fresh = p >= sv.ctx && row0 == 0;  // a drafted row's first pass
           float old = 0.f;
           if (p < total && !fresh) old = wrow[p];
-          if (ok) ok = mbar_wait(&s_score[stream], scores & 1u, s_abort, kTcTimeoutNs);
+          if (ok) ok = tc_wait(&s_score[stream], scores & 1u, s_abort);
           ok = __all_sync(kFullMask, ok);
           ++scores;
           tc_fence_after();
@@ -269,7 +269,7 @@ __global__ void __launch_bounds__(weigh_tc_threads<MX>(), 1)
     uint32_t phase = 0;
     bool ok = true;
     auto wait = [&](uint64_t* bar, uint32_t count) {
-      if (ok) ok = mbar_wait(bar, count & 1u, s_abort, kTcTimeoutNs);
+      if (ok) ok = tc_wait(bar, count & 1u, s_abort);
       ok = __all_sync(kFullMask, ok);
     };
     const uint32_t keys = tc_desc(units, 16), query = tc_desc(smem, 16);

@@ -365,3 +365,52 @@ def test_a_bound_far_above_the_drafts(mx):
     out = sc.attend(d, lse=lse, max_draft=128)
     check_attention(out.double().cpu().numpy(), lse.double().cpu().numpy(), sc.oracle_attention(), 128)
     assert int(d["err"]) == 0
+
+
+# -------------------------------------------------------------- huge scores
+
+@pytest.mark.parametrize("power", [4, 26, 30, 36, 100])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("S, ctx, n", [(1, 700, 1), (1, 700, 20), (1, 700, 50), (160, 90, 20), (160, 140, 50)])
+@pytest.mark.parametrize("mx", [False, True])
+@pytest.mark.parametrize("sign", [1, -1])
+def test_huge_scores(sign, mx, S, ctx, n, D, power):
+    """Scores of any size that floats hold, far apart: the largest wins, wherever it lies, and equal ones share.
+    (All products and sums are exact: one dimension counts, with powers of two and small integers.)  Contexts
+    that many CTAs share, and ones that a CTA has whole."""
+    sc = Scene([ctx] * S, [n] * S, 1, D, 4, 16, mx, "star", seed=600)
+    sc.scale = sign * D ** -0.5 * 1.1
+    d = sc.device()
+    total = ctx + n
+    p = np.arange(total)
+    at = (torch.from_numpy(sc.table[:, p // 16].astype(np.int64)).cuda(), torch.from_numpy(p % 16).cuda())
+    gen = torch.Generator(device="cuda").manual_seed(4)
+    c = torch.randint(-100, 100, (S, total), generator=gen, device="cuda").float() if not mx else \
+        torch.randint(-12, 13, (S, total), generator=gen, device="cuda").float()
+    c[:, [5, ctx - 10]] = 15.0 if mx else 120.0  # the winners, in tiles far apart
+    half = 2.0 ** (power // 2)
+    d["q"].zero_()
+    d["q"][:, :, 0] = half
+    rows = torch.zeros(S, total, 1, D, device="cuda")
+    rows[..., 0, 0] = sign * c
+    if mx:
+        d["kv"][0][at] = rows.to(torch.float8_e4m3fn).view(torch.uint8)
+        d["kv"][1][at] = 127 + power // 2
+    else:
+        d["kv"][0][at] = (rows * half).to(torch.bfloat16)
+    lse = torch.empty(sc.T, sc.HQ, device="cuda")
+    out = sc.attend(d, lse=lse).view(S, n, 4, D)
+    assert int(d["err"]) == 0
+    s = c.double() * 2.0 ** (2 * (power // 2)) * abs(sc.scale)
+    x = s[:, None].expand(S, n, total).clone()
+    x[:, :, ctx:].masked_fill_(~torch.eye(n, dtype=torch.bool, device="cuda"), -float("inf"))
+    prob = x.softmax(-1)
+    v = torch.from_numpy(sc.values(1)).cuda()[at][:, :, 0]
+    want, mag = (prob @ v)[:, :, None], (prob @ v.abs())[:, :, None]
+    # as in tree_util.check_attention; where more than the winners count (the smallest power) the scores are exact
+    # but for the factor scale * log2(e): two roundings each, and those of the difference
+    e = 2.0 ** -22 * float(s.abs().max()) if power < 8 else 0.0
+    bound = 2.0 ** -8 * (want.abs() + mag) * 1.01 + (2.0 ** -11 + 2 * e) * mag
+    assert ((out.double() - want).abs() <= bound).all()
+    ref = torch.logsumexp(x, -1)[:, :, None]
+    assert ((lse.view(S, n, 4).double() - ref).abs() <= 2.0 ** -21 * ref.abs() + 2.0 ** -20).all()
