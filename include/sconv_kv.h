@@ -657,7 +657,9 @@ SCONV_KV_API int sconv_kv_tree_accept_mxfp8(
  *                   not alias weights; out_positions >= min(keep, positions).
  * keep >= 1, sinks and recent >= 0, sinks + recent <= keep, else
  * SCONV_KV_ERR_SHAPE.  Two sequences that share a page (a common prefix) must
- * not be evicted in place: results are then unspecified.
+ * not be evicted in place: results are then unspecified.  The launch is laid
+ * out for sequences as long as the block table and `positions` allow: a
+ * `positions` near the longest context's length makes it fit short ones.
  */
 SCONV_KV_API int sconv_kv_evict(
     const float* weights, int64_t positions, int64_t seq_stride,

@@ -798,7 +798,9 @@ def evict(weights, context_lens, block_table, k_cache, v_cache, sinks, recent, k
     [S, Hkv, positions]; ties to the lower position).  They move to the front in
     their order; kept (int32 [S, Hkv, keep]) gets their old positions (-1
     behind a shorter sequence), new_lens the lengths, weights_out (not
-    weights itself) their weights."""
+    weights itself) their weights.  The launch is laid out for contexts as long
+    as the table and `positions` allow: weights cut to the longest context's
+    length (a view) make it fit short ones."""
     rc = _tree.evict(weights, context_lens, block_table, k_cache, None, v_cache, None, sinks, recent, kept,
                      new_lens, weights_out, err_flag, _on(stream))
     if rc:

@@ -19,9 +19,10 @@
 // same call gives the same bits).
 //
 // Softmax statistics, scores and sums are fp32; the only rounding to fewer bits
-// are the probabilities, to bf16 for the second product (2^-9 relative each,
-// independent, so the output's error stays below its own bf16 rounding), and the
-// output.
+// are the probabilities, to bf16 for the second product (which is what the matrix
+// instruction takes next to bf16 values; 2^-8 relative each at most, independent of one
+// another), and the output.  Measured against 64 bits: 0.0023 relative, where the output's
+// own rounding alone is 0.0017.
 //
 // Masked keys: their score is replaced by -inf before the maximum, and a drafted V row
 // (that nobody or not everybody may see) is cleaned of NaN and infinities before the
@@ -239,7 +240,7 @@ __device__ __noinline__ float restore_nonfinite(const AttendParams& P, int seq, 
 // The K/V bytes bound it: R rows cost 16 of the 512 issue slots that 16 keys'
 // 8 KB take to arrive; what counts is bytes in flight, so the loads of the
 // next step are issued as soon as the registers are free.  Measured: 64 heads' one row over 8192
-// tokens 23 us with the join (latency: range, table, K/V, parts; the bytes take 5).
+// tokens 24 us with the join (latency: range, table, K/V, parts; the bytes take 5).
 
 template <int D, bool MX>
 struct RowsLayout {

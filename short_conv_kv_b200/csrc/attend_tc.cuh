@@ -14,9 +14,10 @@
 // stays in tensor memory and is rescaled only when a row's maximum has grown by
 // more than 2^8.  Tensor memory holds just two S and two O tiles of 128
 // columns, which is what sets two streams and 128 keys a tile.
-// Measured: 32 rows over 1,048,573 tokens 690 us at 1965 MHz (6.2 TB/s; bound by the bytes of K/V), 747 at the
-// power limit; 32 ragged trees of 8 to 64 rows 151 us (4.4 TB/s: a unit's beginning and end); 384 to 512 rows over
-// 12 to 20 thousand MXFP8 tokens 425 us (554 TF/s: the decoding), as bf16 343.
+// Measured: 32 rows over 1,048,573 tokens 640 to 700 us in short runs (6.2 to 6.7 TB/s; bound by the bytes of K/V),
+// 780 to 830 in long ones at the power limit, MXFP8 950 to 1000 (2.3 TB/s: the decoding); 32 ragged trees of 8 to 64
+// rows 150 to 159 us (a unit's beginning and end); 384 to 512 rows over 12 to 20 thousand MXFP8 tokens 412 to 438 us
+// (the decoding), as bf16 327 to 392.  (Ranges: several boxes.)
 #pragma once
 #include "tc.cuh"
 
@@ -249,7 +250,7 @@ __global__ void __launch_bounds__(tc_threads<D, MX>(), 1)
         const int c = tid % (D / 8);
         const uint16_t* qp = P.q + sv.a * P.q_tok + static_cast<int64_t>(h) * P.g * P.q_head + c * 8;
         // rows of zeros up to a whole tile: what lay there would cost power, and so clocks
-        // (32 rows over 1M tokens at the power limit: 820 us with it)
+        // (32 rows over 1M tokens at the power limit, on one box: 820 us with it, 747 without)
         const int fill = pair ? 256 : 128;
         for (int r0 = tid / (D / 8); r0 < fill; r0 += 8 * kStep) {
           uint4 v[8];

@@ -427,9 +427,10 @@ int evict_impl(const float* weights, int64_t positions, int64_t w_seq, int64_t w
   A.recent = recent;
   A.kept = kept;
   A.new_lens = new_lens;
-  // Clusters: as many CTAs a (sequence, head) as fill the GPU, while each has
-  // 2048 positions.  (16 sequences of 8 heads: 2 a selection, 1 a movement, 8 of either for
-  // a single sequence.)
+  // Clusters: as many CTAs a (sequence, head) as fill the GPU, while each has 2048 of the positions that a
+  // sequence can have.  The lengths are on the device, so that is what the block table or the
+  // weights' rows hold, whichever is less, for contexts of any length.  (16 sequences of 8 heads: 2 a
+  // selection, 1 a movement, 8 of either for a single sequence.)
   const int64_t units = static_cast<int64_t>(H) * seqs->num_seqs;
   auto spread = [&](int64_t n, int64_t per) {
     int c = 1;
@@ -438,7 +439,7 @@ int evict_impl(const float* weights, int64_t positions, int64_t w_seq, int64_t w
   };
   {
     const int c = spread(units, 1);
-    // a slice's keys, if they fit
+    // a slice's keys, of such a sequence, if they fit
     const int64_t slice = (A.q.capacity / c + 1025) / 1024 * 1024 + 1024;
     int room = static_cast<int>(std::min<int64_t>(slice, 48 * 1024));
     const void* fn = sconv::evict_select_fn();

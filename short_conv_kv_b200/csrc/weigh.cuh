@@ -5,7 +5,7 @@
 //     weights[i, h, p] += add   (p < ctx),   = add   (a drafted token's row)
 // with the lse that the attention left.  This kernel is for up to 16 query rows
 // a K/V head (64 decode steps over 2355 tokens: 82 us, 3.9 TB/s, weigh_tc.cuh 124; 64 rows over 262,139
-// MXFP8 tokens: 312 us against 139), and for head_dim 256, where a unit of weigh_tc.cuh's ring would take
+// MXFP8 tokens: 312 us against 137), and for head_dim 256, where a unit of weigh_tc.cuh's ring would take
 // 64 KB.  S^T[key, row] = K Q^T: 16 keys a warp
 // and step are the m16 of the matrix instruction, straight from global memory (as
 // in attend_rows_kernel), the query rows its n8 from shared memory, so few

@@ -2,13 +2,13 @@
 // cores, for head_dim 64 and 128.
 //
 // S[key, row] = K Q^T: 128 cache rows are the product's M, the query rows that count (used
-// tokens, packed) its N, so a decode step's few rows cost no padding, and a thread
+// tokens, packed) its N, so ragged row counts cost little padding, and a thread
 // owns a key: it adds up its row of S and updates one weight, with no exchange between
-// threads and no atomics.  Two warpgroups take the tiles in turn, each with its own S in
+// threads and no atomics.  (Up to 16 rows go to weigh.cuh, which has both sides' times.)  Two warpgroups take the tiles in turn, each with its own S in
 // tensor memory (256 columns); the products run two tiles ahead.  K comes through the ring of
-// tc.cuh; more than 256 rows read it again.  A decode step is bound by the bytes of K, many rows
-// by the exponentials and, with MXFP8, by the decoding.  Measured: 64 rows over 262,139 MXFP8 tokens
-// 139 us (2.1 TB/s of codes).
+// tc.cuh; more than 256 rows read it again.  Bound by the bytes of K with few rows, by
+// the exponentials with many and, with MXFP8, by the decoding.  Measured: 64 rows over 262,139 MXFP8 tokens
+// 137 us (2.1 TB/s of codes), as bf16 105 (5.3 TB/s).
 #pragma once
 #include "tc.cuh"
 
